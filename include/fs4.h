@@ -128,6 +128,16 @@ enum {
  * It exists so that the device-side timeout path can be exercised on a GPU. */
 #define FS4_TEST_STALL (1u << 30)
 
+/* Element types of the MXFP4 and Muon entry points. */
+enum { FS4_F32 = 0, FS4_BF16 = 1, FS4_F16 = 2 };
+
+/* Options of the MXFP4 entry points (see fs4_mxfp4_quantize, fs4_mxfp4_gemm). */
+enum {
+  FS4_MX_SCALE_CEIL = 1u << 5, /* block scale: the smallest power of two that saturates nothing */
+  FS4_MX_STOCHASTIC = 1u << 6, /* stochastic rounding of the codes */
+  FS4_MX_ACCUMULATE = 1u << 7  /* products: add to D instead of overwriting it */
+};
+
 /* Upper limits checked on the host. */
 #define FS4_MAX_DIM 65536       /* m, n of one Newton-Schulz matrix */
 #define FS4_MAX_ITERS 32        /* K */
@@ -263,6 +273,83 @@ fs4_status fs4_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const
                           const uint8_t* b_codes, const uint8_t* b_scales, const float* b_sg,
                           int64_t M, int64_t N, int64_t K, float* d, int64_t ldd,
                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------- MXFP4
+ *
+ * The microscaled 4-bit format of the OCP MX specification: E2M1 codes as in NVFP4, one
+ * E8M0 scale byte s (the value 2^(s - 127); 255 is NaN) per 32 consecutive elements of a
+ * row, and no tensor scale: element = code * 2^(s - 127).  Sizes need not be multiples of
+ * anything; a row's last block is completed with zeros.
+ *   - PLAIN: codes[r * ceil(K/2) + c/2], scales[r * ceil(K/32) + c/32]; with K odd the last
+ *     high nibble of a row is 0.
+ *   - TILED: codes as in TILED NVFP4.  Scales: atom (r/128, c/128) of 512 bytes at
+ *     ((r/128)*(Kp/128) + c/128) * 512, rows padded to 128 and columns to Kp =
+ *     roundup(K,256); inside it the scale of row r and of block c/32 is byte
+ *     16*(r%32) + 4*((r%128)/32) + (c/32)%4.  Padding is zero, scales included.
+ *     Sizes: codes Rp*Kp/2 bytes, scales Rp*Kp/32 bytes.
+ * None of these calls synchronises or allocates. */
+
+/* Quantise x (rows x cols of `dtype`: FS4_F32, FS4_BF16 or FS4_F16; leading dimension ld)
+ * into its row view (1x32 blocks along rows, a rows x cols matrix), its column view (the row
+ * view of x^T, a cols x rows matrix), or both in one pass: a view whose codes and scales are
+ * null is not written.  With amax the largest |x| of a block:
+ *   scale   2^e with e = floor(log2 amax) - 2 (the MX specification's rule: codes of values
+ *           over 6 2^e saturate), or with FS4_MX_SCALE_CEIL the smallest e with
+ *           amax <= 6 2^e; e >= -127, and -127 for amax = 0.
+ *   codes   sign | RN_e2m1(|x| 2^-e), ties to even; signed zeros keep their sign.  With
+ *           FS4_MX_STOCHASTIC, |x| 2^-e between the grid values lo and hi goes up when
+ *           u <= (v - lo) / (hi - lo): u = (f + 1/2) 2^-16, f the 16-bit field c % 4
+ *           (lowest first) of SplitMix64 at count r * ceil(K/4) + c/4 (see
+ *           fs4_momentum_nvfp4) for element (r, c) of a view with K columns, from `seed`
+ *           for the row view and seed ^ 0xD1B54A32D192ED03 for the column view.
+ *   A block holding NaN or Inf gets scale 255 and zero codes, so every value read from it,
+ *   and every product with it, is NaN.
+ * flags: FS4_LAYOUT_TILED (both views), FS4_MX_SCALE_CEIL, FS4_MX_STOCHASTIC.  One launch.
+ * Errors: FS4_ERR_INVALID_ARG (null x, no view, half a view, unknown type or flag, ld < cols,
+ * codes or scales not 16-byte aligned, x not aligned to its type), FS4_ERR_SHAPE (rows or
+ * cols outside [1, 2^31]), FS4_ERR_ALIAS, FS4_ERR_ARCH, FS4_ERR_CUDA. */
+fs4_status fs4_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                              uint8_t* row_codes, uint8_t* row_scales, uint8_t* col_codes,
+                              uint8_t* col_scales, uint32_t flags, uint64_t seed, void* stream);
+
+/* The values of a rows x cols MXFP4 matrix (PLAIN, or TILED with FS4_LAYOUT_TILED) in y
+ * (`dtype`, leading dimension ld), each rounded once.  BF16 and FP32 hold every value
+ * exactly.  One launch.  Errors as fs4_mxfp4_quantize. */
+fs4_status fs4_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                int64_t cols, void* y, int32_t dtype, int64_t ld, uint32_t flags,
+                                void* stream);
+
+/* D = deq(A) deq(B)^T on the tensor cores (tcgen05 kind::mxf4, FP32 accumulation), A M x K
+ * and B N x K in the TILED layout, D M x N of `d_dtype` with leading dimension ldd, rounded
+ * once.  With FS4_MX_ACCUMULATE D is read first and added to in FP32 (a weight gradient over
+ * micro-batches).  The three products of a linear layer y = x W^T take the views
+ *   y = x_row W_row^T,  dx = dy_row (W_col)^T,  dW = dy_col (x_col)^T.
+ * The workspace (256 bytes, 256-byte aligned) holds the device status word: zero it once;
+ * calls only add to it, so several calls on any streams may share it; fs4_device_status
+ * reads it.  M, N and K in [1, 2^20].  One launch; the result does not depend on timing.
+ * Errors: FS4_ERR_SHAPE, FS4_ERR_INVALID_ARG (null or misaligned pointers, ldd < N, unknown
+ * type or flag), FS4_ERR_ALIAS (D overlaps an operand or the workspace), FS4_ERR_WORKSPACE,
+ * FS4_ERR_ARCH, FS4_ERR_CUDA; FS4_ERR_TIMEOUT in the status word. */
+fs4_status fs4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                          const uint8_t* b_scales, int64_t M, int64_t N, int64_t K, void* d,
+                          int32_t d_dtype, int64_t ldd, uint32_t flags, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace fs4_mxfp4_linear needs for M rows of K elements (0 for sizes outside
+ * its range). */
+size_t fs4_mxfp4_linear_workspace_size(int64_t M, int64_t K);
+
+/* D = Q(x) deq(W)^T: x (M x K of `x_dtype`, leading dimension ldx) is quantised to the MXFP4
+ * row view (nearest; flags may hold FS4_MX_SCALE_CEIL) and multiplied with W (N x K, TILED)
+ * as by fs4_mxfp4_gemm; equal to the two calls bit for bit.  The first 256 bytes of the
+ * workspace are the status word, to be zeroed once; the rest holds Q(x), so calls whose work
+ * overlaps on the GPU need separate workspaces.  flags: FS4_MX_SCALE_CEIL,
+ * FS4_MX_ACCUMULATE.  Errors as fs4_mxfp4_gemm; FS4_ERR_ALIAS also for a workspace or D that
+ * overlaps x, W or the other. */
+fs4_status fs4_mxfp4_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
+                            const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, void* d,
+                            int32_t d_dtype, int64_t ldd, uint32_t flags, void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 /* ----------------------------------------------------------- Newton-Schulz */
 

@@ -7,6 +7,7 @@ streams) into those calls.  There is no CPU or fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Sequence
 
@@ -23,6 +24,8 @@ __all__ = [
     "ns_batched_workspace_size", "ns_layout", "device_status", "tiled_shape", "Fs4Error",
     "momentum_nvfp4", "root_ns_batched_nvfp4", "root_ns_bf16_batched", "ns_bf16_batched_workspace_size",
     "ns_bf16_layout",
+    "mxfp4_quantize", "mxfp4_quantize_both", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_linear",
+    "mxfp4_linear_workspace_size", "mxfp4_tiled_shape",
     "MUON_COEFFS", "stop_after", "FS4_AXIS_ROW", "FS4_AXIS_COL", "FS4_TEST_STALL",
     "FS4_NS_RHT", "FS4_NS_ADAPTIVE46", "FS4_NS_CLIP_QUANTILE",
 ]
@@ -172,6 +175,180 @@ def gemm(a, b, M: int, N: int, K: int, out: torch.Tensor | None = None,
                                     workspace.numel(), _stream(stream)),
           "fs4_nvfp4_gemm")
     return out
+
+
+_DTYPES = {torch.float32: _lib.FS4_F32, torch.bfloat16: _lib.FS4_BF16, torch.float16: _lib.FS4_F16}
+
+
+def _check_matrix(x: torch.Tensor, name: str, device: torch.device | None = None) -> None:
+    if not x.is_cuda or x.dtype not in _DTYPES or x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError(f"{name} must be a CUDA float32, bfloat16 or float16 matrix with unit column stride")
+    if device is not None and x.device != device:
+        raise ValueError(f"{name} is on {x.device}, not on {device}")
+
+
+def _check_bytes(t: torch.Tensor, need: int, name: str, device: torch.device) -> None:
+    if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != device or t.numel() < need:
+        raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {need} bytes on {device}")
+
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """Makes `device` and `stream` (default: the device's current one) current, so that what a
+    call allocates or zeroes belongs to the stream it runs on; yields the stream's handle."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield torch.cuda.current_stream(device).cuda_stream
+
+
+def mxfp4_tiled_shape(rows: int, cols: int) -> tuple[int, int]:
+    """(codes bytes, scales bytes) of a rows x cols MXFP4 matrix in the TILED layout."""
+    rp, cp = _round_up(rows, 128), _round_up(cols, 256)
+    return rp * cp // 2, rp * cp // 32
+
+
+def _mx_sizes(rows: int, cols: int, tiled: bool) -> tuple[int, int]:
+    return mxfp4_tiled_shape(rows, cols) if tiled else (rows * ((cols + 1) // 2), rows * ((cols + 31) // 32))
+
+
+def _mx_view(rows: int, cols: int, tiled: bool, device, out):
+    need = _mx_sizes(rows, cols, tiled)
+    if out is not None:
+        for t, n, name in zip(out, need, ("codes", "scales")):
+            _check_bytes(t, n, name, device)
+        return out
+    shapes = [(n,) for n in need] if tiled else [(rows, (cols + 1) // 2), (rows, (cols + 31) // 32)]
+    return tuple(torch.empty(s, dtype=torch.uint8, device=device) for s in shapes)
+
+
+def _mx_scale_flag(scale_rule: str) -> int:
+    if scale_rule not in ("floor", "ceil"):
+        raise ValueError(f"scale_rule must be 'floor' or 'ceil', not {scale_rule!r}")
+    return _lib.FS4_MX_SCALE_CEIL if scale_rule == "ceil" else 0
+
+
+def _mx_quantize(x, row, col, tiled, scale_rule, seed, handle):
+    flags = _mx_scale_flag(scale_rule) | (FS4_LAYOUT_TILED if tiled else 0)
+    flags |= 0 if seed is None else _lib.FS4_MX_STOCHASTIC
+    rows, cols = x.shape
+    check(_lib.lib().fs4_mxfp4_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, cols, _ld(x),
+                                        *(_ptr(t) for t in (row or (None, None))),
+                                        *(_ptr(t) for t in (col or (None, None))), flags,
+                                        0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF, handle),
+          "fs4_mxfp4_quantize")
+
+
+def mxfp4_quantize(x: torch.Tensor, axis: int = FS4_AXIS_ROW, tiled: bool = False, scale_rule: str = "floor",
+                   seed: int | None = None, out=None, stream=None):
+    """MXFP4-quantise an FP32, BF16 or FP16 matrix (fs4_mxfp4_quantize): its row view, or with
+    FS4_AXIS_COL the row view of x^T.  scale_rule "floor" is the MX specification's, "ceil"
+    saturates nothing; a seed rounds stochastically.  Returns (codes, scales); `out` is such
+    a pair to write into."""
+    _check_matrix(x, "x")
+    if axis not in (FS4_AXIS_ROW, FS4_AXIS_COL):
+        raise ValueError(f"axis must be FS4_AXIS_ROW or FS4_AXIS_COL, not {axis}")
+    rows, cols = x.shape if axis == FS4_AXIS_ROW else reversed(x.shape)
+    with _on(x.device, stream) as handle:
+        view = _mx_view(rows, cols, tiled, x.device, out)
+        row, col = (view, None) if axis == FS4_AXIS_ROW else (None, view)
+        _mx_quantize(x, row, col, tiled, scale_rule, seed, handle)
+    return view
+
+
+def mxfp4_quantize_both(x: torch.Tensor, tiled: bool = False, scale_rule: str = "floor", seed: int | None = None,
+                        out=None, stream=None):
+    """The row view and the column view of x in one pass over it (fs4_mxfp4_quantize), as a
+    training step needs them.  Returns ((codes, scales) of x, (codes, scales) of x^T)."""
+    _check_matrix(x, "x")
+    rows, cols = x.shape
+    with _on(x.device, stream) as handle:
+        row = _mx_view(rows, cols, tiled, x.device, None if out is None else out[0])
+        col = _mx_view(cols, rows, tiled, x.device, None if out is None else out[1])
+        _mx_quantize(x, row, col, tiled, scale_rule, seed, handle)
+    return row, col
+
+
+def _mx_check_operand(op, rows: int, cols: int, tiled: bool, name: str, device) -> None:
+    for t, need, part in zip(op, _mx_sizes(rows, cols, tiled), ("codes", "scales")):
+        _check_bytes(t, need, f"{name} {part}", device)
+
+
+def _mx_out(out, shape, dtype, device):
+    if out is None:
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype must be float32, bfloat16 or float16, not {dtype}")
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check_matrix(out, "out", device)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out must be {shape[0]} x {shape[1]}, got {tuple(out.shape)}")
+    return out
+
+
+def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, tiled: bool = False,
+                     dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values of a rows x cols MXFP4 matrix (fs4_mxfp4_dequantize) in `dtype`, or in `out`."""
+    dev = codes.device
+    _mx_check_operand((codes, scales), rows, cols, tiled, "the matrix's", dev)
+    with _on(dev, stream) as handle:
+        y = _mx_out(out, (rows, cols), dtype, dev)
+        check(_lib.lib().fs4_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, y.data_ptr(),
+                                              _DTYPES[y.dtype], _ld(y), FS4_LAYOUT_TILED if tiled else 0, handle),
+              "fs4_mxfp4_dequantize")
+    return y
+
+
+def mxfp4_gemm(a, b, M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+               accumulate: bool = False, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """D = deq(A) deq(B)^T, or D += with accumulate (fs4_mxfp4_gemm); a and b are (codes,
+    scales) in the TILED layout, A M x K and B N x K.  A workspace of the caller's is zeroed
+    once, before its first call."""
+    dev = a[0].device
+    _mx_check_operand(a, M, K, True, "a", dev)
+    _mx_check_operand(b, N, K, True, "b", dev)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    with _on(dev, stream) as handle:
+        d = _mx_out(out, (M, N), dtype, dev)
+        if workspace is None:
+            workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+        _check_bytes(workspace, 256, "workspace", dev)
+        check(_lib.lib().fs4_mxfp4_gemm(a[0].data_ptr(), a[1].data_ptr(), b[0].data_ptr(), b[1].data_ptr(), M, N, K,
+                                        d.data_ptr(), _DTYPES[d.dtype], _ld(d),
+                                        _lib.FS4_MX_ACCUMULATE if accumulate else 0, workspace.data_ptr(),
+                                        workspace.numel(), handle),
+              "fs4_mxfp4_gemm")
+    return d
+
+
+def mxfp4_linear_workspace_size(M: int, K: int) -> int:
+    return int(_lib.lib().fs4_mxfp4_linear_workspace_size(M, K))
+
+
+def mxfp4_linear(x: torch.Tensor, w, N: int, dtype: torch.dtype | None = None, scale_rule: str = "floor",
+                 out: torch.Tensor | None = None, accumulate: bool = False, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Q(x) deq(W)^T for an FP32, BF16 or FP16 x (M x K) and TILED MXFP4 weights w = (codes,
+    scales), N x K (fs4_mxfp4_linear); in x's type unless dtype or out says otherwise."""
+    _check_matrix(x, "x")
+    M, K = x.shape
+    dev = x.device
+    _mx_check_operand(w, N, K, True, "w", dev)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    flags = _mx_scale_flag(scale_rule) | (_lib.FS4_MX_ACCUMULATE if accumulate else 0)
+    need = mxfp4_linear_workspace_size(M, K)
+    with _on(dev, stream) as handle:
+        d = _mx_out(out, (M, N), x.dtype if dtype is None else dtype, dev)
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+            workspace[:256].zero_()
+        _check_bytes(workspace, need, "workspace", dev)
+        check(_lib.lib().fs4_mxfp4_linear(x.data_ptr(), _DTYPES[x.dtype], M, K, _ld(x), w[0].data_ptr(),
+                                          w[1].data_ptr(), N, d.data_ptr(), _DTYPES[d.dtype], _ld(d), flags,
+                                          workspace.data_ptr(), workspace.numel(), handle),
+              "fs4_mxfp4_linear")
+    return d
 
 
 def _ld(t: torch.Tensor) -> int:

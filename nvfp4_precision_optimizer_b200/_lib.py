@@ -24,6 +24,8 @@ FS4_AXIS_ROW, FS4_AXIS_COL = 0, 1
 FS4_SG_AMAX, FS4_LAYOUT_TILED = 1, 2
 FS4_TEST_STALL = 1 << 30   # test only: a device wait that runs out (see include/fs4.h)
 FS4_NS_RHT, FS4_NS_ADAPTIVE46, FS4_NS_CLIP_QUANTILE = 1 << 2, 1 << 3, 1 << 4
+FS4_F32, FS4_BF16, FS4_F16 = 0, 1, 2
+FS4_MX_SCALE_CEIL, FS4_MX_STOCHASTIC, FS4_MX_ACCUMULATE = 1 << 5, 1 << 6, 1 << 7
 MAX_BATCH = 224
 MAX_ITERS = 32
 
@@ -69,6 +71,14 @@ SIGNATURES = {
     "fs4_nvfp4_dequantize": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_i64, c_u32, c_vp]),
     "fs4_nvfp4_gemm": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp,
                                c_i64, c_vp, c_sz, c_vp]),
+    "fs4_mxfp4_quantize": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_u32,
+                                   ctypes.c_uint64, c_vp]),
+    "fs4_mxfp4_dequantize": (c_i32, [c_vp, c_vp, c_i64, c_i64, c_vp, c_i32, c_i64, c_u32, c_vp]),
+    "fs4_mxfp4_gemm": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_i32, c_i64, c_u32,
+                               c_vp, c_sz, c_vp]),
+    "fs4_mxfp4_linear_workspace_size": (c_sz, [c_i64, c_i64]),
+    "fs4_mxfp4_linear": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp, c_i32, c_i64,
+                                 c_u32, c_vp, c_sz, c_vp]),
     "fs4_root_ns_workspace_size": (c_sz, [c_i64, c_i64]),
     "fs4_root_ns_batched_workspace_size": (c_sz, [c_i32, ctypes.POINTER(NsDesc)]),
     "fs4_root_ns": (c_i32, [c_vp, c_i64, c_i64, c_i64, c_vp, c_i64, c_i32, c_f32, c_f32, c_f32,

@@ -7,6 +7,7 @@
 #include "../../include/fs4.h"
 #include "fs4_device.cuh"
 #include "fs4_internal.h"
+#include "mx_internal.h"
 
 using namespace fs4;
 
@@ -233,6 +234,13 @@ fs4_status run_ns(const Plan& pl, int32_t K, float clip_k, uint32_t flags, const
 }
 
 }  // namespace
+
+fs4_status fs4::current_device(int* num_sms) {
+  DeviceInfo di;
+  const fs4_status s = device_info(&di);
+  *num_sms = di.num_sms;
+  return s;
+}
 
 extern "C" {
 

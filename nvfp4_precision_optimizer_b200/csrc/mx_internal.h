@@ -1,0 +1,41 @@
+// Internal definitions shared by the MXFP4 and Muon kernels and their C entry points.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/fs4.h"
+
+namespace fs4 {
+
+// Element types of the C ABI (fs4_dtype).
+constexpr int kTypeF32 = 0, kTypeBf16 = 1, kTypeF16 = 2;
+inline int64_t type_bytes(int dtype) { return dtype == kTypeF32 ? 4 : 2; }
+
+// The current device's SM count; FS4_ERR_ARCH off sm_100 (api.cu).
+fs4_status current_device(int* num_sms);
+
+// ---------------------------------------------------------------- launchers (mxfp4.cu)
+cudaError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* row_codes,
+                                  uint8_t* row_scales, uint8_t* col_codes, uint8_t* col_scales, bool tiled, bool ceil_rule,
+                                  bool stochastic, uint64_t seed, cudaStream_t st);
+cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* y, int dtype,
+                                    int64_t ld, bool tiled, cudaStream_t st, int num_sms);
+
+// ---------------------------------------------------------------- launchers (mxfp4_gemm.cu)
+struct MxGemmArgs {
+  const uint8_t* a_codes;
+  const uint8_t* a_scales;
+  const uint8_t* b_codes;
+  const uint8_t* b_scales;
+  int64_t M, N, K;
+  void* d;
+  int64_t ldd;
+  int32_t dtype;
+  int32_t accumulate;
+  uint32_t* status;
+};
+cudaError_t launch_mxfp4_gemm(const MxGemmArgs& a, cudaStream_t st, int num_sms);
+
+}  // namespace fs4

@@ -1,0 +1,235 @@
+"""MXFP4 on the GPU against the 64-bit oracle: quantisation byte for byte, products within a
+derived bound.
+
+Bound of a product: a code times a code and its power of two are exact, so the only error before
+the one rounding of the output is FP32 accumulation of K terms, at most K 2^-23 sum |a b|."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mxfp4 as O
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+HALF_STEP = {t: torch.finfo(t).eps / 2 for t in TYPES.values()}
+SHAPES = [(1, 1), (1, 33), (3, 64), (31, 31), (33, 257), (128, 256), (129, 130), (200, 515), (257, 96)]
+
+
+def make(rows, cols, dtype, seed=0):
+    g = torch.Generator().manual_seed(1000 * rows + cols + seed)
+    x = torch.randn(rows, cols, generator=g) * torch.exp2(torch.randint(-6, 7, (rows, 1), generator=g).float())
+    return x.to(dtype)
+
+
+def np64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def same(view, want, tiled):
+    codes, scales = (O.pack_tiled if tiled else O.pack_plain)(*want)
+    np.testing.assert_array_equal(view[1].cpu().numpy(), scales)
+    np.testing.assert_array_equal(view[0].cpu().numpy(), codes)
+
+
+@pytest.mark.parametrize("tiled", (False, True), ids=("plain", "tiled"))
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_quantize_matches_the_oracle(fs4, shape, kind, tiled):
+    x = make(*shape, TYPES[kind])
+    for rule in ("floor", "ceil"):
+        for seed in (None, 77):
+            row = O.quantize(np64(x), rule, seed)
+            col = O.quantize(np64(x).T, rule, None if seed is None else seed ^ O.COLUMN_SEED)
+            kw = dict(tiled=tiled, scale_rule=rule, seed=seed)
+            both = fs4.mxfp4_quantize_both(x.cuda(), **kw)
+            same(both[0], row, tiled)
+            same(both[1], col, tiled)
+            same(fs4.mxfp4_quantize(x.cuda(), **kw), row, tiled)
+            same(fs4.mxfp4_quantize(x.cuda(), axis=fs4.FS4_AXIS_COL, **kw), col, tiled)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_quantize_extremes(fs4, kind):
+    """Zeros of either sign, subnormals, the largest values, ties, and blocks with NaN or Inf."""
+    t = TYPES[kind]
+    f = torch.finfo(t)
+    x = torch.zeros(6, 96, dtype=t)
+    x[0, 5] = -0.0
+    x[1, :6] = torch.tensor([f.max, -f.max, f.tiny, f.smallest_normal, f.max / 4, -f.max / 16]).to(t)
+    x[2, 32:40] = torch.tensor([6.0, 5.0, 3.5, 2.5, 1.75, 1.25, 0.75, 0.25]).to(t)
+    x[3, 64:67] = torch.tensor([f.tiny / 4, -f.tiny / 2, f.tiny / 8]).to(t)
+    x[4, 3], x[4, 40], x[5, 95] = float("nan"), float("inf"), float("-inf")
+    for seed in (None, 3):
+        row, col = fs4.mxfp4_quantize_both(x.cuda(), seed=seed)
+        same(row, O.quantize(np64(x), "floor", seed), False)
+        same(col, O.quantize(np64(x).T, "floor", None if seed is None else seed ^ O.COLUMN_SEED), False)
+        y = fs4.mxfp4_dequantize(*row, 6, 96, dtype=t).cpu()
+        want = O.values(*O.quantize(np64(x), "floor", seed))
+        with np.errstate(over="ignore"):
+            assert torch.equal(torch.nan_to_num(y, nan=1.5), torch.nan_to_num(torch.from_numpy(want).to(t), nan=1.5))
+            assert (torch.isnan(y).numpy() == np.isnan(want)).all()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_dequantize_reads_back_every_layout(fs4, shape, kind):
+    x = make(*shape, torch.float32)
+    want = torch.from_numpy(O.values(*O.quantize(np64(x)))).to(TYPES[kind])
+    for tiled in (False, True):
+        view = fs4.mxfp4_quantize(x.cuda(), tiled=tiled)
+        assert torch.equal(fs4.mxfp4_dequantize(*view, *shape, tiled=tiled, dtype=TYPES[kind]).cpu(), want)
+        wide = torch.full((shape[0], shape[1] + 3), 7.0, dtype=TYPES[kind], device="cuda")
+        fs4.mxfp4_dequantize(*view, *shape, tiled=tiled, out=wide[:, 1:-2])
+        assert torch.equal(wide[:, 1:-2].cpu(), want) and (wide[:, 0] == 7).all() and (wide[:, -2:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_quantize_strided_and_unaligned_input(fs4, kind):
+    big = make(70, 300, TYPES[kind]).cuda()
+    for x in (big[3:60, 1:258], big[::2, 8:200], big[:, 5:6], big[4:5]):
+        plain = x.cpu().contiguous()
+        row, col = fs4.mxfp4_quantize_both(x)
+        same(row, O.quantize(np64(plain)), False)
+        same(col, O.quantize(np64(plain).T), False)
+
+
+def test_quantize_past_32_bit_offsets(fs4):
+    """2.2e9 elements: the last rows come out as they do on their own."""
+    rows, cols = 67_000, 33_000
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x.copy_(torch.arange(cols, device="cuda").remainder(97) - 48.0)
+    x[-256:] = torch.randn(256, cols, device="cuda").bfloat16()
+    codes, scales = fs4.mxfp4_quantize(x)
+    part = fs4.mxfp4_quantize(x[-200:].contiguous())
+    assert torch.equal(codes[-200:], part[0]) and torch.equal(scales[-200:], part[1])
+    y = fs4.mxfp4_dequantize(codes, scales, rows, cols, dtype=torch.bfloat16)
+    assert torch.equal(y[-200:], fs4.mxfp4_dequantize(*part, 200, cols, dtype=torch.bfloat16))
+
+
+def operand(fs4, rows, k, seed):
+    x = make(rows, k, torch.float32, seed).clamp(-300, 300)
+    return fs4.mxfp4_quantize(x.cuda(), tiled=True), O.values(*O.quantize(np64(x)))
+
+
+PRODUCTS = [(1, 1, 1), (1, 16, 32), (1, 300, 700), (7, 129, 257), (16, 128, 2048), (17, 520, 300), (33, 65, 64), (64, 1000, 1536),
+            (65, 40, 515), (128, 128, 256), (130, 257, 1000), (300, 16, 2100), (513, 300, 130), (256, 512, 4096), (700, 1100, 96)]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("size", PRODUCTS, ids=str)
+def test_gemm_against_float64(fs4, size, kind):
+    M, N, K = size
+    t = TYPES[kind]
+    (a, av), (b, bv) = operand(fs4, M, K, 1), operand(fs4, N, K, 2)
+    scale = 2.0 ** -8          # keeps the FP16 products finite; exact
+    av = av * scale
+    a = (a[0], torch.where(a[1] == 0, a[1], a[1] - 8))
+    want = av @ bv.T
+    bound = K * 2.0 ** -23 * (np.abs(av) @ np.abs(bv).T)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    got = np64(fs4.mxfp4_gemm(a, b, M, N, K, dtype=t, workspace=ws))
+    tiny = float(torch.finfo(t).smallest_normal) * float(torch.finfo(t).eps)
+    assert (np.abs(got - want) <= bound + HALF_STEP[t] * (np.abs(want) + bound) + tiny).all()
+    # added to D in place, in a strided D whose other columns stay as they are
+    wide = torch.randn(M, N + 5, device="cuda").to(t)
+    before = wide.clone()
+    fs4.mxfp4_gemm(a, b, M, N, K, out=wide[:, 2:-3], accumulate=True, workspace=ws)
+    total = want + np64(before[:, 2:-3])
+    assert (np.abs(np64(wide[:, 2:-3]) - total) <= bound + 2.0 ** -24 * np.abs(total) + HALF_STEP[t] * (np.abs(total) + bound) + tiny).all()
+    assert torch.equal(wide[:, :2], before[:, :2]) and torch.equal(wide[:, -3:], before[:, -3:])
+    assert fs4.device_status(ws) == 0
+
+
+@pytest.mark.parametrize("size", [(1, 256, 512), (40, 130, 300), (300, 140, 300)], ids=str)
+def test_gemm_nan_blocks_reach_their_rows_and_no_others(fs4, size):
+    M, N, K = size
+    x = make(M, K, torch.float32)
+    w = make(N, K, torch.float32, 1)
+    x[M // 2, 7] = float("inf")
+    w[N // 3, K - 1] = float("nan")
+    y = fs4.mxfp4_gemm(fs4.mxfp4_quantize(x.cuda(), tiled=True), fs4.mxfp4_quantize(w.cuda(), tiled=True), M, N, K, dtype=torch.float32)
+    want = torch.zeros(M, N, dtype=torch.bool)
+    want[M // 2], want[:, N // 3] = True, True
+    assert torch.equal(torch.isnan(y).cpu(), want)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("size", [(1, 200, 513), (9, 64, 4096), (16, 300, 33), (33, 48, 700), (140, 260, 384)], ids=str)
+def test_linear_is_quantise_then_product(fs4, size, kind):
+    M, N, K = size
+    x = make(M, K + 3, TYPES[kind]).cuda()[:, 1:-2]
+    w = fs4.mxfp4_quantize(make(N, K, torch.float32, 3).cuda() / 64, tiled=True)
+    for rule in ("floor", "ceil"):
+        want = fs4.mxfp4_gemm(fs4.mxfp4_quantize(x, tiled=True, scale_rule=rule), w, M, N, K, dtype=TYPES[kind])
+        assert torch.equal(fs4.mxfp4_linear(x, w, N, scale_rule=rule), want)
+    ws = torch.zeros(fs4.mxfp4_linear_workspace_size(M, K), dtype=torch.uint8, device="cuda")
+    d = torch.ones(M, N, device="cuda")
+    fs4.mxfp4_linear(x, w, N, out=d, accumulate=True, workspace=ws)
+    f32 = fs4.mxfp4_linear(x, w, N, dtype=torch.float32, workspace=ws)
+    assert torch.equal(d, f32 + 1.0) and fs4.device_status(ws) == 0
+    x[M - 1, 0] = float("nan")
+    y = fs4.mxfp4_linear(x, w, N)
+    assert torch.isnan(y[M - 1]).all() and not torch.isnan(y[:M - 1]).any()
+
+
+def test_calls_repeat_bit_for_bit_on_streams_and_in_graphs(fs4):
+    x = make(20, 2048, torch.bfloat16).cuda()
+    w = fs4.mxfp4_quantize(make(400, 2048, torch.float32, 4).cuda(), tiled=True)
+    want = fs4.mxfp4_linear(x, w, 400)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [fs4.mxfp4_linear(x, w, 400, stream=s) for s in (side, None, side, None)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    ws = torch.zeros(fs4.mxfp4_linear_workspace_size(20, 2048), dtype=torch.uint8, device="cuda")
+    out = torch.zeros(20, 400, dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fs4.mxfp4_linear(x, w, 400, out=out, workspace=ws)
+    x.mul_(2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, fs4.mxfp4_linear(x, w, 400))
+
+
+def test_three_products_of_a_linear_layer(fs4):
+    """y = x W^T, dx = dy W, dW += dy^T x on quantised operands, against the oracle's operands."""
+    T, n_in, n_out = 200, 300, 170
+    x, w, dy = make(T, n_in, torch.bfloat16).cuda(), make(n_out, n_in, torch.float32, 1).cuda(), make(T, n_out, torch.bfloat16, 2).cuda()
+    xr, xc = fs4.mxfp4_quantize_both(x, tiled=True)
+    wr, wc = fs4.mxfp4_quantize_both(w, tiled=True)
+    gr, gc = fs4.mxfp4_quantize_both(dy, tiled=True, seed=9)
+    val = lambda t, seed=None: O.values(*O.quantize(t, "floor", seed))  # noqa: E731
+    X, W, G = np64(x), np64(w), np64(dy)
+    dw = torch.ones(n_out, n_in, device="cuda")
+    for got, left, right, k, plus in (
+            (fs4.mxfp4_gemm(xr, wr, T, n_out, n_in, dtype=torch.float32), val(X), val(W), n_in, 0.0),
+            (fs4.mxfp4_gemm(gr, wc, T, n_in, n_out, dtype=torch.float32), val(G, 9), val(W.T), n_out, 0.0),
+            (fs4.mxfp4_gemm(gc, xc, n_out, n_in, T, out=dw, accumulate=True), val(G.T, 9 ^ O.COLUMN_SEED), val(X.T), T, 1.0)):
+        want = left @ right.T + plus
+        bound = (k + 2) * 2.0 ** -23 * (np.abs(left) @ np.abs(right).T + plus)
+        assert (np.abs(np64(got) - want) <= bound).all()
+
+
+def test_refusals_on_device(fs4):
+    x = torch.zeros(8, 64, device="cuda")
+    view = fs4.mxfp4_quantize(x, tiled=True)
+    with pytest.raises(ValueError):
+        fs4.mxfp4_quantize(x.t())
+    with pytest.raises(ValueError):
+        fs4.mxfp4_quantize(x.double())
+    with pytest.raises(ValueError):
+        fs4.mxfp4_quantize(x[0])
+    with pytest.raises(ValueError):
+        fs4.mxfp4_gemm(view, view, 129, 8, 64)                   # more rows than the operand has
+    with pytest.raises(ValueError):
+        fs4.mxfp4_gemm(view, view, 8, 8, 64, accumulate=True)
+    with pytest.raises(ValueError):
+        fs4.mxfp4_gemm(view, view, 8, 8, 64, out=torch.zeros(8, 9, device="cuda"))
+    with pytest.raises(ValueError):
+        fs4.mxfp4_dequantize(view[0][:10], view[1], 8, 64, tiled=True)
+    with pytest.raises(ValueError):
+        fs4.mxfp4_linear(x, view, 8, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(fs4.Fs4Error):
+        fs4.mxfp4_dequantize(view[0][:8192].view(-1), view[0][8192:], 8, 64, out=view[0].view(torch.float32)[:512].view(8, 64))
