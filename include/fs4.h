@@ -502,6 +502,64 @@ fs4_status fs4_root_ns_bf16_batched_timed(int32_t count, const fs4_ns_desc* desc
 
 
 
+/* -------------------------------------------------------------------- Muon
+ *
+ * The Newton-Schulz step of Section 2 "Root optimizer" at working precision, as the Muon
+ * optimizer takes it, for matrices of any size in [1, FS4_MAX_DIM]^2: no quantisation and no
+ * clip.  Where fs4_root_ns and fs4_root_ns_bf16_batched trade accuracy for 4-bit or BF16
+ * operands, this step is meant to be exact to the BF16 rounding of its result:
+ *   X_0 = U / (||U||_F + 1e-7) (transposed when rows > cols), then K times
+ *   A = X X^T, B = b A + c A^2, X <- a X + B X,
+ * with FP16 tensor-core operands, FP32 accumulation and FP32 diagonals of A and B kept out
+ * of the operands.  With the Muon coefficients and K = 5 the result is 0.3-1.3e-3 (relative,
+ * Frobenius) from the exact iteration; it repeats bit for bit.  A zero matrix gives zero.  A
+ * matrix with NaN or Inf in U is carried as zeros (its update is zero) and recorded as
+ * FS4_ERR_NONFINITE in the status word; so is a result that is not finite, as coefficients
+ * that make the iteration diverge give. */
+
+enum { FS4_MUON_NESTEROV = 1u << 0 };
+
+/* One matrix of a Muon call, rows x cols with leading dimensions, every array of its own type
+ * (FS4_F32, FS4_BF16, FS4_F16): g the gradient (or the update to orthogonalise), m the
+ * momentum, updated (fs4_muon_step) or null (fs4_muon_orthogonalize), w the weights, updated,
+ * or the result.  scale multiplies X_K. */
+typedef struct {
+  void* w;
+  const void* g;
+  void* m;
+  int64_t rows, cols, ld_w, ld_g, ld_m;
+  int32_t w_dtype, g_dtype, m_dtype;
+  float scale;
+} fs4_muon_desc;
+
+/* Workspace bytes of a call on `count` matrices (HOST arrays of sizes; 0 if a size or count
+ * is out of range). */
+size_t fs4_muon_workspace_size(int32_t count, const int64_t* rows, const int64_t* cols);
+
+/* w = scale X_K of U = g for every matrix (descs: HOST array), in 2 + 3K launches over all of
+ * them.  coeffs: HOST array of n_coeffs triples (a, b, c), one for all iterations or one for
+ * each (n_coeffs = 1 or K); |a|, |b|, |c| <= 16.
+ *   Errors: FS4_ERR_SHAPE (count outside [1, FS4_MAX_BATCH], K outside [1, FS4_MAX_ITERS], a
+ *   size), FS4_ERR_INVALID_ARG (null or misaligned pointers, leading dimensions, types,
+ *   coefficients, scale), FS4_ERR_ALIAS (an output overlaps an input, another output or the
+ *   workspace), FS4_ERR_WORKSPACE, FS4_ERR_ARCH, FS4_ERR_CUDA; FS4_ERR_NONFINITE and
+ *   FS4_ERR_TIMEOUT in the status word, which each call resets.  Calls whose work overlaps on
+ *   the GPU need separate workspaces. */
+fs4_status fs4_muon_orthogonalize(int32_t count, const fs4_muon_desc* descs, int32_t K,
+                                  const float* coeffs, int32_t n_coeffs, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* The whole optimizer step on every matrix, in place:
+ *   m <- beta m + (1 - beta) g         (in FP32, rounded to m's type)
+ *   U = m, or with FS4_MUON_NESTEROV  beta m + (1 - beta) g  from the stored m
+ *   w <- (1 - lr weight_decay) w - lr scale X_K      (in FP32, rounded to w's type)
+ * lr >= 0, 0 <= beta < 1.  Errors as fs4_muon_orthogonalize; a matrix with NaN or Inf keeps
+ * its weights but for the decay (its momentum is updated as stated). */
+fs4_status fs4_muon_step(int32_t count, const fs4_muon_desc* descs, int32_t K,
+                         const float* coeffs, int32_t n_coeffs, double lr, double beta,
+                         double weight_decay, uint32_t flags, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------ no-alloc variant */
 
 /* Bytes of the workspace array built into the library for fs4_root_ns_noalloc. */

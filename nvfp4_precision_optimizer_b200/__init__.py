@@ -26,6 +26,7 @@ __all__ = [
     "ns_bf16_layout",
     "mxfp4_quantize", "mxfp4_quantize_both", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_linear",
     "mxfp4_linear_workspace_size", "mxfp4_tiled_shape",
+    "muon_orthogonalize", "muon_step", "muon_workspace_size",
     "MUON_COEFFS", "stop_after", "FS4_AXIS_ROW", "FS4_AXIS_COL", "FS4_TEST_STALL",
     "FS4_NS_RHT", "FS4_NS_ADAPTIVE46", "FS4_NS_CLIP_QUANTILE",
 ]
@@ -349,6 +350,91 @@ def mxfp4_linear(x: torch.Tensor, w, N: int, dtype: torch.dtype | None = None, s
                                           workspace.data_ptr(), workspace.numel(), handle),
               "fs4_mxfp4_linear")
     return d
+
+
+def muon_workspace_size(shapes: Sequence[tuple[int, int]]) -> int:
+    """Workspace bytes of muon_orthogonalize and muon_step on matrices of these shapes."""
+    n = len(shapes)
+    rows, cols = (c_i64s(*(int(s[i]) for s in shapes)) for i, c_i64s in ((0, ctypes.c_int64 * n), (1, ctypes.c_int64 * n)))
+    return int(_lib.lib().fs4_muon_workspace_size(n, rows, cols))
+
+
+def _muon_coeffs(coeffs, K: int):
+    """(ctypes array of (a, b, c) triples, their number): one triple, or one per iteration."""
+    flat = [float(v) for v in coeffs] if not hasattr(coeffs[0], "__len__") else [float(v) for t in coeffs for v in t]
+    if len(flat) not in (3, 3 * K):
+        raise ValueError(f"coeffs must be one (a, b, c) or K = {K} of them")
+    return (ctypes.c_float * len(flat))(*flat), len(flat) // 3
+
+
+def _muon_call(ws_list, gs, ms, scales, K, coeffs, workspace, stream, step):
+    n, dev = len(gs), gs[0].device
+    arr = (_lib.MuonDesc * n)()
+    for i, (w, g) in enumerate(zip(ws_list, gs)):
+        m = ms[i] if ms is not None else None
+        arr[i] = _lib.MuonDesc(w.data_ptr(), g.data_ptr(), _ptr(m), g.shape[0], g.shape[1], _ld(w), _ld(g),
+                               0 if m is None else _ld(m), _DTYPES[w.dtype], _DTYPES[g.dtype],
+                               0 if m is None else _DTYPES[m.dtype], scales[i])
+    c, nc = _muon_coeffs(coeffs, K)
+    need = muon_workspace_size([g.shape for g in gs])
+    if workspace is not None:
+        _check_bytes(workspace, need, "workspace", dev)
+    else:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    if step is None:
+        check(_lib.lib().fs4_muon_orthogonalize(n, arr, K, c, nc, workspace.data_ptr(), workspace.numel(), stream),
+              "fs4_muon_orthogonalize")
+    else:
+        check(_lib.lib().fs4_muon_step(n, arr, K, c, nc, *step, workspace.data_ptr(), workspace.numel(), stream),
+              "fs4_muon_step")
+
+
+def muon_orthogonalize(Gs: Sequence[torch.Tensor], K: int = 5, coeffs=MUON_COEFFS, dtype: torch.dtype = torch.bfloat16,
+                       outs: Sequence[torch.Tensor] | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Orthogonalise a list of FP32, BF16 or FP16 matrices of any sizes by K Newton-Schulz
+    iterations (fs4_muon_orthogonalize), in `dtype` or into `outs`.  coeffs is one (a, b, c)
+    or one per iteration.  Accurate to BF16: about 1e-3 of the exact iteration."""
+    if not Gs:
+        return []
+    dev = Gs[0].device
+    for i, G in enumerate(Gs):
+        _check_matrix(G, f"Gs[{i}]", dev)
+    if outs is not None and len(outs) != len(Gs):
+        raise ValueError(f"{len(outs)} outs for {len(Gs)} matrices")
+    with _on(dev, stream) as handle:
+        outs = [_mx_out(None if outs is None else outs[i], G.shape, dtype, dev) for i, G in enumerate(Gs)]
+        _muon_call(outs, Gs, None, [1.0] * len(Gs), K, coeffs, workspace, handle, None)
+    return outs
+
+
+def _muon_scale(scale, rows: int, cols: int) -> float:
+    if scale == "rms":
+        return 0.2 * max(rows, cols) ** 0.5
+    if scale == "spectral":
+        return max(1.0, rows / cols) ** 0.5
+    return float(scale)
+
+
+def muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], momenta: Sequence[torch.Tensor], lr: float,
+              beta: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0, K: int = 5, coeffs=MUON_COEFFS,
+              scale="rms", workspace: torch.Tensor | None = None, stream=None) -> None:
+    """One Muon step on every matrix, in place (fs4_muon_step): momentum, orthogonalised
+    direction, decoupled weight decay, weights.  Each tensor is FP32, BF16 or FP16.  scale:
+    "rms" multiplies the direction by 0.2 sqrt(max(rows, cols)), "spectral" by
+    sqrt(max(1, rows / cols)); or a number."""
+    if not (len(params) == len(grads) == len(momenta)):
+        raise ValueError("params, grads and momenta must be lists of one length")
+    if not params:
+        return
+    dev = params[0].device
+    for i, ts in enumerate(zip(params, grads, momenta)):
+        for t, name in zip(ts, ("params", "grads", "momenta")):
+            _check_matrix(t, f"{name}[{i}]", dev)
+            if t.shape != ts[0].shape:
+                raise ValueError(f"{name}[{i}] must have the shape of params[{i}], {tuple(ts[0].shape)}")
+    with _on(dev, stream) as handle:
+        _muon_call(params, grads, momenta, [_muon_scale(scale, *p.shape) for p in params], K, coeffs, workspace, handle,
+                   (lr, beta, weight_decay, _lib.FS4_MUON_NESTEROV if nesterov else 0))
 
 
 def _ld(t: torch.Tensor) -> int:

@@ -25,6 +25,7 @@ FS4_SG_AMAX, FS4_LAYOUT_TILED = 1, 2
 FS4_TEST_STALL = 1 << 30   # test only: a device wait that runs out (see include/fs4.h)
 FS4_NS_RHT, FS4_NS_ADAPTIVE46, FS4_NS_CLIP_QUANTILE = 1 << 2, 1 << 3, 1 << 4
 FS4_F32, FS4_BF16, FS4_F16 = 0, 1, 2
+FS4_MUON_NESTEROV = 1
 FS4_MX_SCALE_CEIL, FS4_MX_STOCHASTIC, FS4_MX_ACCUMULATE = 1 << 5, 1 << 6, 1 << 7
 MAX_BATCH = 224
 MAX_ITERS = 32
@@ -47,6 +48,12 @@ class Nvfp4State(ctypes.Structure):
 class QuantDesc(ctypes.Structure):
     _fields_ = [("x", c_vp), ("rows", c_i64), ("cols", c_i64), ("ld", c_i64), ("axis", c_i32),
                 ("codes", c_vp), ("scales", c_vp), ("s_g", c_vp)]
+
+
+class MuonDesc(ctypes.Structure):
+    _fields_ = [("w", c_vp), ("g", c_vp), ("m", c_vp), ("rows", c_i64), ("cols", c_i64), ("ld_w", c_i64),
+                ("ld_g", c_i64), ("ld_m", c_i64), ("w_dtype", c_i32), ("g_dtype", c_i32), ("m_dtype", c_i32),
+                ("scale", c_f32)]
 
 
 class NsLayout(ctypes.Structure):
@@ -79,6 +86,11 @@ SIGNATURES = {
     "fs4_mxfp4_linear_workspace_size": (c_sz, [c_i64, c_i64]),
     "fs4_mxfp4_linear": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp, c_i32, c_i64,
                                  c_u32, c_vp, c_sz, c_vp]),
+    "fs4_muon_workspace_size": (c_sz, [c_i32, ctypes.POINTER(c_i64), ctypes.POINTER(c_i64)]),
+    "fs4_muon_orthogonalize": (c_i32, [c_i32, ctypes.POINTER(MuonDesc), c_i32, ctypes.POINTER(c_f32), c_i32, c_vp,
+                                       c_sz, c_vp]),
+    "fs4_muon_step": (c_i32, [c_i32, ctypes.POINTER(MuonDesc), c_i32, ctypes.POINTER(c_f32), c_i32, ctypes.c_double,
+                              ctypes.c_double, ctypes.c_double, c_u32, c_vp, c_sz, c_vp]),
     "fs4_root_ns_workspace_size": (c_sz, [c_i64, c_i64]),
     "fs4_root_ns_batched_workspace_size": (c_sz, [c_i32, ctypes.POINTER(NsDesc)]),
     "fs4_root_ns": (c_i32, [c_vp, c_i64, c_i64, c_i64, c_vp, c_i64, c_i32, c_f32, c_f32, c_f32,

@@ -1,0 +1,182 @@
+// C entry points of the Muon step (declared in include/fs4.h): argument checks, workspace plan
+// and the launch sequence.
+#include <cmath>
+#include <cstring>
+
+#include "fs4_device.cuh"
+#include "muon_internal.h"
+
+using namespace fs4;
+
+namespace {
+
+inline bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+inline bool known_type(int32_t t) { return t == FS4_F32 || t == FS4_BF16 || t == FS4_F16; }
+inline int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+
+struct Range {
+  uintptr_t lo, hi;
+};
+inline Range range_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t type) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + (uintptr_t)(((rows - 1) * ld + cols) * type_bytes(type))};
+}
+inline bool meets(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+bool shape_ok(int64_t m, int64_t n) { return m >= 1 && n >= 1 && m <= FS4_MAX_DIM && n <= FS4_MAX_DIM; }
+
+int64_t parts_of(int64_t m, int64_t n) {
+  const int64_t rows = kMuonUnit / n > 1 ? kMuonUnit / n : 1;      // rows of one partial sum
+  return (m + rows - 1) / rows;
+}
+
+// [header | partial sums | one block per matrix]
+int64_t plan(int32_t count, const int64_t* rows, const int64_t* cols, MuonParams* p) {
+  int64_t parts = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (p) {
+      p->mat[i].partial = parts;
+      p->mat[i].parts = (int32_t)parts_of(rows[i], cols[i]);
+    }
+    parts += parts_of(rows[i], cols[i]);
+  }
+  int64_t off = up(kMuonHeader + 8 * parts, 1024);
+  for (int32_t i = 0; i < count; ++i) {
+    const int64_t m = rows[i] < cols[i] ? rows[i] : cols[i], n = rows[i] < cols[i] ? cols[i] : rows[i];
+    if (p) p->mat[i].base = off;
+    off = up(off + (m <= kMuonThin ? thin_bytes(m, n) : muon_layout(up(m, kMuonPad), up(n, kMuonPad)).end), 1024);
+  }
+  return off;
+}
+
+bool fill_prefix(MuonParams& p, int64_t (*units)(const MuonMat&)) {
+  int64_t acc = 0;
+  p.prefix[0] = 0;
+  for (int i = 0; i < p.count; ++i) {
+    acc += units(p.mat[i]);
+    if (acc > 0x7FFFFFFF) return false;
+    p.prefix[i + 1] = (int32_t)acc;
+  }
+  return true;
+}
+
+thread_local MuonParams t_muon;   // 20 KB: too large for every caller's stack
+
+fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, const float* coeffs, int32_t n_coeffs, double lr,
+               double beta, double weight_decay, uint32_t flags, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!descs || !coeffs) return FS4_ERR_INVALID_ARG;
+  if (count < 1 || count > kMuonMaxBatch || K < 1 || K > FS4_MAX_ITERS) return FS4_ERR_SHAPE;
+  if (n_coeffs != 1 && n_coeffs != K) return FS4_ERR_INVALID_ARG;
+  if (flags & ~(uint32_t)(step ? FS4_MUON_NESTEROV : 0u)) return FS4_ERR_INVALID_ARG;
+  // the FP16 operands hold |A| and |B| up to 255
+  for (int32_t i = 0; i < 3 * n_coeffs; ++i)
+    if (!(std::fabs(coeffs[i]) <= 16.0f)) return FS4_ERR_INVALID_ARG;
+  if (step && (!std::isfinite(lr) || lr < 0.0 || !(beta >= 0.0 && beta < 1.0) || !std::isfinite(weight_decay)))
+    return FS4_ERR_INVALID_ARG;
+  MuonParams& p = t_muon;
+  std::memset(&p, 0, sizeof(p));
+  p.count = count;
+  static thread_local int64_t rows[kMuonMaxBatch], cols[kMuonMaxBatch];
+  static thread_local Range out[2 * kMuonMaxBatch], in[kMuonMaxBatch];
+  int32_t outs = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const fs4_muon_desc& d = descs[i];
+    if (!d.w || !d.g || (step ? !d.m : d.m != nullptr)) return FS4_ERR_INVALID_ARG;
+    if (!shape_ok(d.rows, d.cols)) return FS4_ERR_SHAPE;
+    if (!known_type(d.w_dtype) || !known_type(d.g_dtype) || (step && !known_type(d.m_dtype)) || !std::isfinite(d.scale))
+      return FS4_ERR_INVALID_ARG;
+    if (d.ld_w < d.cols || d.ld_g < d.cols || (step && d.ld_m < d.cols)) return FS4_ERR_INVALID_ARG;
+    const int64_t most = INT64_MAX / 4 / d.rows;
+    if (d.ld_w > most || d.ld_g > most || (step && d.ld_m > most)) return FS4_ERR_INVALID_ARG;
+    if (!aligned(d.w, type_bytes(d.w_dtype)) || !aligned(d.g, type_bytes(d.g_dtype)) || (step && !aligned(d.m, type_bytes(d.m_dtype))))
+      return FS4_ERR_INVALID_ARG;
+    MuonMat& m = p.mat[i];
+    m.g = d.g; m.mom = step ? d.m : nullptr; m.w = d.w;
+    m.ldg = d.ld_g; m.ldm = d.ld_m; m.ldw = d.ld_w;
+    m.tg = (int8_t)d.g_dtype; m.tm = (int8_t)(step ? d.m_dtype : 0); m.tw = (int8_t)d.w_dtype;
+    m.scale = d.scale;
+    m.tall = d.rows > d.cols;
+    m.m = (int32_t)(m.tall ? d.cols : d.rows);
+    m.n = (int32_t)(m.tall ? d.rows : d.cols);
+    m.mp = (int32_t)up(m.m, kMuonPad);
+    m.np = (int32_t)up(m.n, kMuonPad);
+    rows[i] = d.rows;
+    cols[i] = d.cols;
+    in[i] = range_of(d.g, d.rows, d.cols, d.ld_g, d.g_dtype);
+    out[outs++] = range_of(d.w, d.rows, d.cols, d.ld_w, d.w_dtype);
+    if (step) out[outs++] = range_of(d.m, d.rows, d.cols, d.ld_m, d.m_dtype);
+  }
+  const int64_t need = plan(count, rows, cols, &p);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < (size_t)need) return FS4_ERR_WORKSPACE;
+  const Range ws{reinterpret_cast<uintptr_t>(workspace), reinterpret_cast<uintptr_t>(workspace) + (uintptr_t)need};
+  for (int32_t i = 0; i < outs; ++i) {
+    if (meets(out[i], ws)) return FS4_ERR_ALIAS;
+    for (int32_t k = 0; k < count; ++k)
+      if (meets(out[i], in[k])) return FS4_ERR_ALIAS;
+    for (int32_t k = i + 1; k < outs; ++k)
+      if (meets(out[i], out[k])) return FS4_ERR_ALIAS;
+  }
+  for (int32_t k = 0; k < count; ++k)
+    if (meets(in[k], ws)) return FS4_ERR_ALIAS;
+  int sms = 0;
+  const fs4_status ds = current_device(&sms);
+  if (ds != FS4_OK) return ds;
+
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  p.ws = static_cast<uint8_t*>(workspace);
+  p.status = static_cast<uint32_t*>(workspace);
+  p.partials = reinterpret_cast<double*>(p.ws + kMuonHeader);
+  p.nesterov = (flags & FS4_MUON_NESTEROV) ? 1 : 0;
+  p.beta = (float)beta;
+  p.rest = (float)(1.0 - beta);
+  p.rate = step ? (float)lr : -1.0f;
+  p.keep = step ? (float)(1.0 - lr * weight_decay) : 0.0f;
+  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return FS4_ERR_CUDA;
+  // thin matrices need no norm (their Gram matrix has it), so no pass of their own without a momentum
+  if (!fill_prefix(p, [](const MuonMat& m) { return m.m > kMuonThin || m.mom ? (int64_t)m.parts : 0; })) return FS4_ERR_SHAPE;
+  if (p.prefix[count] && launch_muon_moment(p, st, sms) != cudaSuccess) return FS4_ERR_CUDA;
+  if (!fill_prefix(p, [](const MuonMat& m) { return m.m <= kMuonThin ? thin_chunks(m.n) : 0; })) return FS4_ERR_SHAPE;
+  if (p.prefix[count]) {
+    MuonCoeffs mc{K, n_coeffs, {}};
+    std::memcpy(mc.v, coeffs, sizeof(float) * 3 * n_coeffs);
+    if (launch_muon_thin(p, mc, st) != cudaSuccess) return FS4_ERR_CUDA;
+  }
+  if (!fill_prefix(p, [](const MuonMat& m) { return m.m > kMuonThin ? (int64_t)(m.mp / 128) * (m.np / 64) : 0; })) return FS4_ERR_SHAPE;
+  if (!p.prefix[count]) return FS4_OK;
+  if (launch_muon_prepare(p, st, sms) != cudaSuccess) return FS4_ERR_CUDA;
+  for (int32_t k = 0; k < K; ++k) {
+    const float* c = coeffs + (n_coeffs == 1 ? 0 : 3 * k);
+    p.a = c[0]; p.b = c[1]; p.c = c[2];
+    p.slot = k & 1;
+    p.last = k == K - 1;
+    if (!fill_prefix(p, [](const MuonMat& m) { const int64_t T = m.m > kMuonThin ? m.mp / 256 : 0; return T * (T + 1) / 2; })) return FS4_ERR_SHAPE;
+    if (launch_muon_product(MuonProduct::GramX, p, st, sms) != cudaSuccess) return FS4_ERR_CUDA;
+    if (launch_muon_product(MuonProduct::GramA, p, st, sms) != cudaSuccess) return FS4_ERR_CUDA;
+    if (!fill_prefix(p, [](const MuonMat& m) { return m.m > kMuonThin ? (int64_t)(m.mp / 256) * (m.np / 256) : 0; })) return FS4_ERR_SHAPE;
+    if (launch_muon_product(MuonProduct::Update, p, st, sms) != cudaSuccess) return FS4_ERR_CUDA;
+  }
+  return FS4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fs4_muon_workspace_size(int32_t count, const int64_t* rows, const int64_t* cols) {
+  if (count < 1 || count > kMuonMaxBatch || !rows || !cols) return 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (!shape_ok(rows[i], cols[i])) return 0;
+  return (size_t)plan(count, rows, cols, nullptr);
+}
+
+fs4_status fs4_muon_orthogonalize(int32_t count, const fs4_muon_desc* descs, int32_t K, const float* coeffs, int32_t n_coeffs,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  return run(count, descs, false, K, coeffs, n_coeffs, 0.0, 0.0, 0.0, 0u, workspace, workspace_bytes, stream);
+}
+
+fs4_status fs4_muon_step(int32_t count, const fs4_muon_desc* descs, int32_t K, const float* coeffs, int32_t n_coeffs, double lr,
+                         double beta, double weight_decay, uint32_t flags, void* workspace, size_t workspace_bytes, void* stream) {
+  return run(count, descs, true, K, coeffs, n_coeffs, lr, beta, weight_decay, flags, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,102 @@
+// Element access shared by the Muon kernels: values of any of the three types, the update
+// direction, and the owner of a work unit.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "muon_internal.h"
+#include "mx_device.cuh"
+
+namespace fs4 {
+
+__device__ __forceinline__ int owner_of(const int32_t* prefix, int count, int32_t u) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float get1(const void* p, int64_t i, int type) {
+  if (type == kTypeF32) return static_cast<const float*>(p)[i];
+  if (type == kTypeBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+// Round to the type and back: what a later read sees.
+__device__ __forceinline__ float put1(void* p, int64_t i, int type, float v) {
+  if (type == kTypeF32) {
+    static_cast<float*>(p)[i] = v;
+    return v;
+  }
+  if (type == kTypeBf16) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(v);
+    static_cast<__nv_bfloat16*>(p)[i] = h;
+    return __bfloat162float(h);
+  }
+  const __half h = __float2half_rn(v);
+  static_cast<__half*>(p)[i] = h;
+  return __half2float(h);
+}
+
+__device__ __forceinline__ bool aligned16(const void* p, int64_t ld, int type) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * (type == kTypeF32 ? 4 : 2))) & 15) == 0;
+}
+
+// Eight consecutive elements from index i (16-byte aligned).
+__device__ __forceinline__ void get8(const void* p, int64_t i, int type, float* v) {
+  if (type == kTypeF32) {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = f[0], b = f[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    return;
+  }
+  const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (type == kTypeBf16) {
+      v[2 * k] = __uint_as_float(u[k] << 16);
+      v[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+    } else {
+      v[2 * k] = half_lo(u[k]);
+      v[2 * k + 1] = half_hi(u[k]);
+    }
+  }
+}
+// Store and replace by what was stored.
+__device__ __forceinline__ void put8(void* p, int64_t i, int type, float* v) {
+  if (type == kTypeF32) {
+    float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    f[0] = make_float4(v[0], v[1], v[2], v[3]);
+    f[1] = make_float4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+  uint32_t u[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (type == kTypeBf16) {
+      u[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+      v[2 * k] = __uint_as_float(u[k] << 16);
+      v[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+    } else {
+      const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+      u[k] = *reinterpret_cast<const uint32_t*>(&h);
+      v[2 * k] = half_lo(u[k]);
+      v[2 * k + 1] = half_hi(u[k]);
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+__device__ __forceinline__ float direction(const MuonParams& p, float mom, float g) {
+  return p.nesterov ? fmaf(p.beta, mom, p.rest * g) : mom;
+}
+
+// Update direction at (r, c) of G.
+__device__ __forceinline__ float direction_at(const MuonParams& p, const MuonMat& d, int64_t r, int64_t c) {
+  const float g = get1(d.g, r * d.ldg + c, d.tg);
+  return d.mom ? direction(p, get1(d.mom, r * d.ldm + c, d.tm), g) : g;
+}
+
+}  // namespace fs4

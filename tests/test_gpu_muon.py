@@ -1,0 +1,229 @@
+"""The Muon step on the GPU against the 64-bit oracle.
+
+The contract is accuracy to BF16: at most 2^-9 (Frobenius, relative) from the exact iteration
+before the output's own rounding, which adds at most half a step of its type."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mxfp4 as MX
+from oracle import muon as O
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+NEAR = 2.0 ** -9
+SHAPES = [(1, 1), (1, 40), (40, 1), (2, 3), (16, 16), (31, 33), (128, 256), (257, 255), (300, 1111), (1030, 129), (513, 520)]
+
+
+def half_step(t):
+    return torch.finfo(t).eps / 2
+
+
+def make(m, n, dtype=torch.float32, seed=0, rank=None):
+    g = torch.Generator().manual_seed(7919 * m + n + seed)
+    x = torch.randn(m, n, generator=g)
+    if rank:
+        x = 0.05 * x + torch.randn(m, rank, generator=g) @ torch.randn(rank, n, generator=g)
+    return (0.02 * x).to(dtype)
+
+
+def np64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def far(got, want):
+    return np.linalg.norm(np64(got) - want) / np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_orthogonalize_against_float64(fs4, shape, kind):
+    G = make(*shape, TYPES[kind])
+    want = O.orthogonalize(np64(G))
+    ws = torch.empty(fs4.muon_workspace_size([shape]), dtype=torch.uint8, device="cuda")
+    for t in TYPES.values():
+        out = fs4.muon_orthogonalize([G.cuda()], dtype=t, workspace=ws)[0]
+        assert out.dtype == t and out.shape == G.shape
+        assert far(out, want) <= NEAR + half_step(t)
+        assert fs4.device_status(ws) == 0
+
+
+@pytest.mark.parametrize("rank", (1, 16, 64))
+@pytest.mark.parametrize("shape", [(200, 200), (256, 700), (900, 300)], ids=str)
+def test_orthogonalize_low_rank(fs4, shape, rank):
+    G = make(*shape, rank=rank)
+    assert far(fs4.muon_orthogonalize([G.cuda()], dtype=torch.float32)[0], O.orthogonalize(np64(G))) <= NEAR
+
+
+def test_products_one_iteration_at_a_time(fs4):
+    """Each term of the polynomial on its own, over several 256-blocks in each direction."""
+    G = make(600, 1300)
+    for coeffs in ((1.0, 0.0, 0.0), (0.0, 1.0, 0.0), (0.0, 0.0, 1.0), (0.5, -2.0, 1.0)):
+        want = O.orthogonalize(np64(G), 1, coeffs)
+        got = fs4.muon_orthogonalize([G.cuda()], K=1, coeffs=coeffs, dtype=torch.float32)[0]
+        # operands rounded to FP16 enter the result at most five times (X once, or A0 twice and X)
+        assert far(got, want) <= (2.0 ** -20 if coeffs[1:] == (0.0, 0.0) else 5 * 2.0 ** -12), coeffs
+    per = [O.MUON, (1.5, -0.5, 0.0), (1.875, -1.25, 0.375)]
+    assert far(fs4.muon_orthogonalize([G.cuda()], K=3, coeffs=per, dtype=torch.float32)[0], O.orthogonalize(np64(G), 3, per)) <= NEAR
+
+
+def test_many_iterations_reach_the_polar_factor(fs4):
+    G = make(300, 500)
+    u, _, vt = np.linalg.svd(np64(G), full_matrices=False)
+    got = fs4.muon_orthogonalize([G.cuda()], K=20, coeffs=(1.875, -1.25, 0.375), dtype=torch.float32)[0]
+    assert far(got, u @ vt) <= NEAR
+
+
+def test_batch_is_each_matrix_alone_bit_for_bit(fs4):
+    Gs = [make(*s, t).cuda() for s, t in zip(SHAPES, [torch.float32, torch.bfloat16, torch.float16] * 4)]
+    batch = fs4.muon_orthogonalize(Gs)
+    again = fs4.muon_orthogonalize(Gs)
+    for G, b, a in zip(Gs, batch, again):
+        assert torch.equal(b, a) and torch.equal(b, fs4.muon_orthogonalize([G])[0])
+
+
+def test_strided_inputs_and_outputs(fs4):
+    big = make(400, 900, torch.bfloat16).cuda()
+    for G in (big[3:300, 5:705], big[::2, 8:520], big[:, :17], big[5:6]):
+        want = fs4.muon_orthogonalize([G.contiguous()])[0]
+        wide = torch.full((G.shape[0], G.shape[1] + 9), 3.0, dtype=torch.bfloat16, device="cuda")
+        fs4.muon_orthogonalize([G], outs=[wide[:, 4:-5]])
+        assert torch.equal(wide[:, 4:-5], want) and (wide[:, :4] == 3).all() and (wide[:, -5:] == 3).all()
+
+
+def test_zero_tiny_and_huge_updates(fs4):
+    G = make(60, 90)
+    want = fs4.muon_orthogonalize([G.cuda()])[0]
+    assert not fs4.muon_orthogonalize([torch.zeros(60, 90, device="cuda")])[0].any()
+    for scale in (2.0 ** 60, 2.0 ** 100):
+        assert torch.equal(fs4.muon_orthogonalize([G.cuda() * scale])[0], fs4.muon_orthogonalize([G.cuda() * 2.0 ** 30])[0])
+    assert far(want, np64(fs4.muon_orthogonalize([G.cuda() * 2.0 ** 30])[0])) <= 2 * NEAR
+    # the 1e-7 beside a small norm
+    assert far(fs4.muon_orthogonalize([G.cuda() * 1e-8], dtype=torch.float32)[0], O.orthogonalize(np64(G * 1e-8))) <= NEAR
+
+
+def test_nonfinite_matrix_is_reported_and_harms_no_other(fs4):
+    shapes = [(40, 70), (300, 200), (64, 64)]
+    Gs = [make(*s).cuda() for s in shapes]
+    want = fs4.muon_orthogonalize(Gs)
+    for bad in (float("nan"), float("inf")):
+        Gs[1][299, 3] = bad
+        ws = torch.empty(fs4.muon_workspace_size(shapes), dtype=torch.uint8, device="cuda")
+        got = fs4.muon_orthogonalize(Gs, workspace=ws)
+        assert fs4.device_status(ws) == -7
+        assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2]) and not got[1].any()
+        w = [torch.ones(s, device="cuda") for s in shapes]
+        m = [torch.zeros(s, device="cuda") for s in shapes]
+        fs4.muon_step(w, Gs, m, lr=0.5, weight_decay=0.5, workspace=ws)
+        assert fs4.device_status(ws) == -7 and (w[1] == 0.75).all() and not (w[0] == 0.75).all()
+    fs4.muon_orthogonalize([Gs[0]], workspace=ws)
+    assert fs4.device_status(ws) == 0
+    # a diverging iteration is reported too
+    fs4.muon_orthogonalize([Gs[0]], K=8, coeffs=(16.0, 16.0, 16.0), workspace=ws)
+    assert fs4.device_status(ws) == -7
+
+
+@pytest.mark.parametrize("nesterov", (False, True))
+@pytest.mark.parametrize("types", [("f32", "f32", "f32"), ("f32", "bf16", "f32"), ("bf16", "bf16", "bf16"), ("f16", "f16", "f16"),
+                                   ("bf16", "f32", "f16")], ids=str)
+def test_step_against_float64(fs4, types, nesterov):
+    tw, tg, tm = (TYPES[t] for t in types)
+    shapes = [(96, 200), (333, 77), (1, 65), (512, 512)]
+    lr, beta, wd = 0.02, 0.9, 0.1
+    W, G, M = ([make(*s, t, k).mul(f).cuda() for s in shapes] for t, k, f in ((tw, 1, 2.0), (tg, 2, 1.0), (tm, 3, 0.5)))
+    W0, G0, M0 = ([np64(t) for t in ts] for ts in (W, G, M))
+    ws = torch.empty(fs4.muon_workspace_size(shapes), dtype=torch.uint8, device="cuda")
+    fs4.muon_step(W, G, M, lr=lr, beta=beta, nesterov=nesterov, weight_decay=wd, workspace=ws)
+    assert fs4.device_status(ws) == 0
+    for w, m, w0, g0, m0 in zip(W, M, W0, G0, M0):
+        new = beta * m0 + (1 - beta) * g0
+        # beta and 1 - beta rounded, one product and one fused sum: four roundings
+        size = beta * np.abs(m0) + (1 - beta) * np.abs(g0)
+        tiny = float(torch.finfo(tm).smallest_normal) * float(torch.finfo(tm).eps)
+        assert (np.abs(np64(m) - new) <= 4 * 2.0 ** -24 * size + half_step(tm) * (np.abs(new) + 4 * 2.0 ** -24 * size) + tiny).all()
+        kept = np64(m)
+        x = O.orthogonalize(beta * kept + (1 - beta) * g0 if nesterov else kept)
+        step = lr * 0.2 * max(w0.shape) ** 0.5 * x
+        want = (1 - lr * wd) * w0 - step
+        error = np.linalg.norm(np64(w) - want)
+        assert error <= (NEAR + 2.0 ** -22) * np.linalg.norm(step) + (half_step(tw) + 2.0 ** -22) * np.linalg.norm(want)
+
+
+def test_step_scales(fs4):
+    for shape in ((30, 120), (120, 30)):
+        G = make(*shape).cuda()
+        x = fs4.muon_orthogonalize([G], dtype=torch.float32)[0]
+        for scale, f in (("spectral", max(1.0, shape[0] / shape[1]) ** 0.5), ("rms", 0.2 * 120 ** 0.5), (3.0, 3.0)):
+            w, m = torch.zeros(shape, device="cuda"), torch.zeros(shape, device="cuda")
+            fs4.muon_step([w], [G], [m], lr=0.25, beta=0.0, nesterov=False, scale=scale)
+            assert far(w, np64(x) * -0.25 * f) <= 2.0 ** -20
+
+
+def test_streams_and_graphs(fs4):
+    shapes = [(100, 300), (520, 64)]
+    G = [make(*s, torch.bfloat16).cuda() for s in shapes]
+    want = fs4.muon_orthogonalize(G)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    runs = [fs4.muon_orthogonalize(G, stream=s) for s in (side, None, side)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for r in runs for a, b in zip(r, want))
+    W, M = ([torch.zeros(s, device="cuda") for s in shapes] for _ in range(2))
+    W2, M2 = ([t.clone() for t in ts] for ts in (W, M))
+    ws = torch.zeros(fs4.muon_workspace_size(shapes), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fs4.muon_step(W, G, M, lr=0.1, workspace=ws)
+    for _ in range(3):
+        graph.replay()
+        fs4.muon_step(W2, G, M2, lr=0.1)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(W + M, W2 + M2))
+
+
+def test_refusals_on_device(fs4):
+    G, W = torch.zeros(8, 16, device="cuda"), torch.zeros(8, 16, device="cuda")
+    with pytest.raises(ValueError):
+        fs4.muon_orthogonalize([G.t()[:, :3].t().t()])
+    with pytest.raises(ValueError):
+        fs4.muon_orthogonalize([G], outs=[torch.zeros(8, 15, device="cuda")])
+    with pytest.raises(ValueError):
+        fs4.muon_step([W], [G[:, :8]], [torch.zeros(8, 16, device="cuda")], 0.1)
+    with pytest.raises(ValueError):
+        fs4.muon_orthogonalize([G], workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(fs4.Fs4Error):
+        fs4.muon_step([W], [G], [W], 0.1)                      # momentum and weights in one place
+    with pytest.raises(fs4.Fs4Error):
+        fs4.muon_orthogonalize([G], outs=[G])
+    with pytest.raises(fs4.Fs4Error):
+        fs4.muon_step([W], [G], [torch.zeros(8, 16, device="cuda")], 0.1, beta=1.5)
+
+
+def test_training_step_in_four_bits(fs4):
+    """One linear layer: quantise, forward, both gradients, Muon, quantise the new weights."""
+    T, n_in, n_out, lr = 160, 130, 270, 0.05
+    x, dy = make(T, n_in, torch.bfloat16, 1).mul(50).cuda(), make(T, n_out, torch.bfloat16, 2).mul(50).cuda()
+    w = make(n_out, n_in, torch.float32, 3).cuda()
+    m, dw = torch.zeros_like(w), torch.zeros_like(w)
+    W0 = np64(w)
+    xr, xc = fs4.mxfp4_quantize_both(x, tiled=True)
+    wr, wc = fs4.mxfp4_quantize_both(w, tiled=True)
+    gr, gc = fs4.mxfp4_quantize_both(dy, tiled=True, seed=1)
+    y = fs4.mxfp4_linear(x, wr, n_out)
+    dx = fs4.mxfp4_gemm(gr, wc, T, n_in, n_out)
+    fs4.mxfp4_gemm(gc, xc, n_out, n_in, T, out=dw, accumulate=True)
+    fs4.muon_step([w], [dw], [m], lr=lr)
+    wr2, _ = fs4.mxfp4_quantize_both(w, tiled=True)
+
+    val = lambda t, seed=None: MX.values(*MX.quantize(t, "floor", seed))  # noqa: E731
+    X, G = np64(x), np64(dy)
+    step = torch.finfo(torch.bfloat16).eps / 2 + 2.0 ** -15
+    assert far(y, val(X) @ val(W0).T) <= step
+    assert far(dx, val(G, 1) @ val(W0.T).T) <= step
+    want = val(G.T, 1 ^ MX.COLUMN_SEED) @ val(X.T).T
+    assert far(dw, want) <= T * 2.0 ** -23 * 4
+    moved = W0 - lr * 0.2 * max(w.shape) ** 0.5 * O.orthogonalize(want)
+    assert np.linalg.norm(np64(w) - moved) <= (NEAR + 2.0 ** -15) * np.linalg.norm(moved - W0) + 2.0 ** -23 * np.linalg.norm(moved)
+    codes, scales = MX.pack_tiled(*MX.quantize(np64(w)))
+    assert np.array_equal(wr2[0].cpu().numpy(), codes) and np.array_equal(wr2[1].cpu().numpy(), scales)

@@ -1,0 +1,103 @@
+"""CPU checks of the Muon step: the oracle on closed forms, refusals and planning of the C ABI."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import muon as O
+
+
+@pytest.fixture(scope="module")
+def F():
+    import nvfp4_precision_optimizer_b200 as F
+    F._lib.lib()
+    return F
+
+
+def test_oracle_acts_on_singular_values():
+    rng = np.random.default_rng(0)
+    q1, _ = np.linalg.qr(rng.standard_normal((12, 7)))
+    q2, _ = np.linalg.qr(rng.standard_normal((7, 7)))
+    s = np.linspace(0.1, 2.0, 7)
+    want = s / np.sqrt((s * s).sum())
+    for a, b, c in [O.MUON, (1.5, -0.5, 0.0)] * 3:
+        want = a * want + b * want ** 3 + c * want ** 5
+    got = O.orthogonalize(q1 * s @ q2.T, 6, [O.MUON, (1.5, -0.5, 0.0)] * 3)
+    np.testing.assert_allclose(got, q1 * want @ q2.T, atol=1e-7)
+
+
+def test_diagonals_out_of_the_operands_is_the_same_iteration():
+    """A^2 and a X + B X with the diagonals taken out and added back, as the kernels do."""
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((6, 9))
+    A = x @ x.T
+    d = np.diag(A)
+    A0 = A - np.diag(d)
+    np.testing.assert_allclose(A0 @ A0 + A0 * (d[:, None] + d[None]) + np.diag(d * d), A @ A)
+    e = np.diag(A @ A)
+    np.testing.assert_allclose((2.0 + e)[:, None] * x + (A @ A - np.diag(e)) @ x, 2.0 * x + A @ A @ x)
+
+
+def _desc(F, base, rows=32, cols=48, step=True, **kw):
+    d = F._lib.MuonDesc(base, base + (1 << 28), base + (2 << 28) if step else None, rows, cols, cols, cols, cols, 0, 1, 0, 1.0)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def test_refusals(F):
+    lib = F._lib.lib()
+    one = (ctypes.c_float * 3)(*O.MUON)
+    size = lambda *s: F.muon_workspace_size(list(s))  # noqa: E731
+    need, ws, base = size((32, 48)), 1 << 40, 1 << 32
+
+    def step(count=1, K=5, coeffs=one, nc=1, lr=1e-3, beta=0.9, wd=0.0, flags=1, w=ws, nbytes=need, descs=None, **kw):
+        arr = (F._lib.MuonDesc * 1)(_desc(F, base, **kw)) if descs is None else descs
+        return lib.fs4_muon_step(count, arr, K, coeffs, nc, lr, beta, wd, flags, w, nbytes, None)
+
+    for bad in (dict(w=None), dict(g=None), dict(m=None), dict(ld_w=47), dict(ld_g=1), dict(ld_m=0), dict(w_dtype=3), dict(g_dtype=-1),
+                dict(m_dtype=9), dict(scale=float("nan")), dict(ld_w=1 << 62)):
+        if bad == dict(w=None):
+            arr = (F._lib.MuonDesc * 1)(_desc(F, base))
+            arr[0].w = None
+            assert step(descs=arr) == -1
+            continue
+        assert step(**bad) == -1, bad
+    assert step(rows=0) == -2 and step(cols=65537, ld_w=65537, ld_g=65537, ld_m=65537) == -2
+    assert step(count=0) == -2 and step(count=225) == -2 and step(K=0) == -2 and step(K=33) == -2
+    assert step(nc=2) == -1 and step(coeffs=(ctypes.c_float * 3)(17.0, 0, 0)) == -1
+    assert step(coeffs=(ctypes.c_float * 3)(float("nan"), 0, 0)) == -1
+    assert step(lr=-1.0) == -1 and step(lr=float("inf")) == -1 and step(beta=1.0) == -1 and step(beta=-0.1) == -1
+    assert step(wd=float("nan")) == -1 and step(flags=2) == -1
+    assert step(w=None) == -4 and step(w=ws + 128) == -4 and step(nbytes=need - 1) == -4
+    assert step(w=base - need // 256 * 256 + 1024) == -3                       # workspace over the weights
+    arr = (F._lib.MuonDesc * 1)(_desc(F, base))
+    arr[0].g = arr[0].w
+    assert step(descs=arr) == -3
+    arr = (F._lib.MuonDesc * 2)(_desc(F, base), _desc(F, base + (5 << 28)))
+    arr[1].w = arr[0].m
+    assert lib.fs4_muon_step(2, arr, 5, one, 1, 1e-3, 0.9, 0.0, 1, ws, size((32, 48), (32, 48)), None) == -3
+    arr = (F._lib.MuonDesc * 1)(_desc(F, base))                                 # a momentum where none belongs
+    assert lib.fs4_muon_orthogonalize(1, arr, 5, one, 1, ws, need, None) == -1
+
+
+def test_workspace_sizes(F):
+    assert F.muon_workspace_size([(0, 4)]) == 0 and F.muon_workspace_size([(4, 65537)]) == 0
+    assert F.muon_workspace_size([(16, 16)] * 225) == 0
+    a, b = F.muon_workspace_size([(300, 1000)]), F.muon_workspace_size([(1000, 300)])
+    # X in three FP16 parts, A in two and B in one, and two diagonals, on sizes padded to 256
+    floor = 6 * 512 * 1024 + 6 * 512 * 512 + 8 * 512
+    assert floor < a <= floor + 4096 and floor < b <= floor + 4096
+
+
+def test_binding_refusals(F):
+    with pytest.raises(ValueError, match="coeffs"):
+        F._muon_coeffs([(1, 2, 3)] * 4, 5)
+    with pytest.raises(ValueError, match="one length"):
+        F.muon_step([torch.zeros(2, 2)], [], [], 0.1)
+    with pytest.raises(ValueError, match="CUDA"):
+        F.muon_orthogonalize([torch.zeros(2, 2)])
+    assert F.muon_orthogonalize([]) == []
+    assert F._muon_scale("spectral", 8, 2) == 2.0 and F._muon_scale("spectral", 2, 8) == 1.0
+    assert F._muon_scale("rms", 25, 4) == 1.0 and F._muon_scale(3, 1, 1) == 3.0
