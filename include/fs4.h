@@ -536,8 +536,8 @@ typedef struct {
  * is out of range). */
 size_t fs4_muon_workspace_size(int32_t count, const int64_t* rows, const int64_t* cols);
 
-/* w = scale X_K of U = g for every matrix (descs: HOST array), in 2 + 3K launches over all of
- * them.  coeffs: HOST array of n_coeffs triples (a, b, c), one for all iterations or one for
+/* w = scale X_K of U = g for every matrix (descs: HOST array), in three launches over all of
+ * them (three more for matrices with 32 rows or columns or fewer).  coeffs: HOST array of n_coeffs triples (a, b, c), one for all iterations or one for
  * each (n_coeffs = 1 or K); |a|, |b|, |c| <= 16.
  *   Errors: FS4_ERR_SHAPE (count outside [1, FS4_MAX_BATCH], K outside [1, FS4_MAX_ITERS], a
  *   size), FS4_ERR_INVALID_ARG (null or misaligned pointers, leading dimensions, types,

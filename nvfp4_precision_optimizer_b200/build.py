@@ -13,7 +13,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libfs4.so")
 SOURCES = ["kernels.cu", "gemm.cu", "momentum.cu", "api.cu", "noalloc.cu",
            "mxfp4.cu", "mxfp4_gemm.cu", "api_mx.cu",
-           "muon.cu", "muon_gemm.cu", "muon_thin.cu", "api_muon.cu"]
+           "muon.cu", "muon_iterate.cu", "muon_thin.cu", "api_muon.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",

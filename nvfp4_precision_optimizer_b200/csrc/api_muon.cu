@@ -26,41 +26,45 @@ inline bool meets(const Range& a, const Range& b) { return a.lo < b.hi && b.lo <
 bool shape_ok(int64_t m, int64_t n) { return m >= 1 && n >= 1 && m <= FS4_MAX_DIM && n <= FS4_MAX_DIM; }
 
 int64_t parts_of(int64_t m, int64_t n) {
-  const int64_t rows = kMuonUnit / n > 1 ? kMuonUnit / n : 1;      // rows of one partial sum
+  const int64_t unit = m * n / kMuonParts > kMuonUnit ? m * n / kMuonParts : kMuonUnit;
+  const int64_t rows = (unit + n - 1) / n;      // rows of one partial sum
   return (m + rows - 1) / rows;
 }
 
-// [header | partial sums | one block per matrix]
-int64_t plan(int32_t count, const int64_t* rows, const int64_t* cols, MuonParams* p) {
+// Bases and partial sums of every matrix; returns the workspace's bytes.
+int64_t plan(int32_t count, const int64_t* rows, const int64_t* cols, MuonTable* t) {
   int64_t parts = 0;
   for (int32_t i = 0; i < count; ++i) {
-    if (p) {
-      p->mat[i].partial = parts;
-      p->mat[i].parts = (int32_t)parts_of(rows[i], cols[i]);
+    if (t) {
+      t->mat[i].partial = parts;
+      t->mat[i].parts = (int32_t)parts_of(rows[i], cols[i]);
     }
     parts += parts_of(rows[i], cols[i]);
   }
-  int64_t off = up(kMuonHeader + 8 * parts, 1024);
+  int64_t off = up(kMuonPartials + 8 * parts, 1024);
   for (int32_t i = 0; i < count; ++i) {
     const int64_t m = rows[i] < cols[i] ? rows[i] : cols[i], n = rows[i] < cols[i] ? cols[i] : rows[i];
-    if (p) p->mat[i].base = off;
+    if (t) t->mat[i].base = off;
     off = up(off + (m <= kMuonThin ? thin_bytes(m, n) : muon_layout(up(m, kMuonPad), up(n, kMuonPad)).end), 1024);
   }
   return off;
 }
 
-bool fill_prefix(MuonParams& p, int64_t (*units)(const MuonMat&)) {
-  int64_t acc = 0;
-  p.prefix[0] = 0;
-  for (int i = 0; i < p.count; ++i) {
-    acc += units(p.mat[i]);
-    if (acc > 0x7FFFFFFF) return false;
-    p.prefix[i + 1] = (int32_t)acc;
+// Work units of a matrix in each kernel.  Thin matrices need no norm (their Gram matrix has
+// it), so no pass of their own without a momentum.
+int64_t units_of(const MuonMat& m, int kind) {
+  const bool thin = m.m <= kMuonThin;
+  const int64_t T = m.mp / 256;
+  switch (kind) {
+    case kUnitsMoment: return !thin || m.mom ? m.parts : 0;
+    case kUnitsThin: return thin ? thin_chunks(m.n) : 0;
+    case kUnitsPrepare: return thin ? 0 : (int64_t)(m.mp / 128) * (m.np / 64);
+    case kUnitsGram: return thin ? 0 : T * (T + 1) / 2;
+    default: return thin ? 0 : T * (m.np / 256);
   }
-  return true;
 }
 
-thread_local MuonParams t_muon;   // 20 KB: too large for every caller's stack
+thread_local MuonTable t_table;   // 25 KB: too large for every caller's stack
 
 fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, const float* coeffs, int32_t n_coeffs, double lr,
                double beta, double weight_decay, uint32_t flags, void* workspace, size_t workspace_bytes, void* stream) {
@@ -73,9 +77,7 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
     if (!(std::fabs(coeffs[i]) <= 16.0f)) return FS4_ERR_INVALID_ARG;
   if (step && (!std::isfinite(lr) || lr < 0.0 || !(beta >= 0.0 && beta < 1.0) || !std::isfinite(weight_decay)))
     return FS4_ERR_INVALID_ARG;
-  MuonParams& p = t_muon;
-  std::memset(&p, 0, sizeof(p));
-  p.count = count;
+  MuonTable& t = t_table;
   static thread_local int64_t rows[kMuonMaxBatch], cols[kMuonMaxBatch];
   static thread_local Range out[2 * kMuonMaxBatch], in[kMuonMaxBatch];
   int32_t outs = 0;
@@ -90,7 +92,7 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
     if (d.ld_w > most || d.ld_g > most || (step && d.ld_m > most)) return FS4_ERR_INVALID_ARG;
     if (!aligned(d.w, type_bytes(d.w_dtype)) || !aligned(d.g, type_bytes(d.g_dtype)) || (step && !aligned(d.m, type_bytes(d.m_dtype))))
       return FS4_ERR_INVALID_ARG;
-    MuonMat& m = p.mat[i];
+    MuonMat& m = t.mat[i];
     m.g = d.g; m.mom = step ? d.m : nullptr; m.w = d.w;
     m.ldg = d.ld_g; m.ldm = d.ld_m; m.ldw = d.ld_w;
     m.tg = (int8_t)d.g_dtype; m.tm = (int8_t)(step ? d.m_dtype : 0); m.tw = (int8_t)d.w_dtype;
@@ -106,7 +108,7 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
     out[outs++] = range_of(d.w, d.rows, d.cols, d.ld_w, d.w_dtype);
     if (step) out[outs++] = range_of(d.m, d.rows, d.cols, d.ld_m, d.m_dtype);
   }
-  const int64_t need = plan(count, rows, cols, &p);
+  const int64_t need = plan(count, rows, cols, &t);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < (size_t)need) return FS4_ERR_WORKSPACE;
   const Range ws{reinterpret_cast<uintptr_t>(workspace), reinterpret_cast<uintptr_t>(workspace) + (uintptr_t)need};
   for (int32_t i = 0; i < outs; ++i) {
@@ -123,37 +125,31 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
   if (ds != FS4_OK) return ds;
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  p.ws = static_cast<uint8_t*>(workspace);
-  p.status = static_cast<uint32_t*>(workspace);
-  p.partials = reinterpret_cast<double*>(p.ws + kMuonHeader);
-  p.nesterov = (flags & FS4_MUON_NESTEROV) ? 1 : 0;
-  p.beta = (float)beta;
-  p.rest = (float)(1.0 - beta);
-  p.rate = step ? (float)lr : -1.0f;
-  p.keep = step ? (float)(1.0 - lr * weight_decay) : 0.0f;
-  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return FS4_ERR_CUDA;
-  // thin matrices need no norm (their Gram matrix has it), so no pass of their own without a momentum
-  if (!fill_prefix(p, [](const MuonMat& m) { return m.m > kMuonThin || m.mom ? (int64_t)m.parts : 0; })) return FS4_ERR_SHAPE;
-  if (p.prefix[count] && launch_muon_moment(p, st, sms) != cudaSuccess) return FS4_ERR_CUDA;
-  if (!fill_prefix(p, [](const MuonMat& m) { return m.m <= kMuonThin ? thin_chunks(m.n) : 0; })) return FS4_ERR_SHAPE;
-  if (p.prefix[count]) {
-    MuonCoeffs mc{K, n_coeffs, {}};
-    std::memcpy(mc.v, coeffs, sizeof(float) * 3 * n_coeffs);
-    if (launch_muon_thin(p, mc, st) != cudaSuccess) return FS4_ERR_CUDA;
+  for (int kind = 0; kind < kUnitKinds; ++kind) {
+    int64_t acc = 0;
+    t.prefix[kind][0] = 0;
+    for (int32_t i = 0; i < count; ++i) {
+      acc += units_of(t.mat[i], kind);
+      if (acc > 0x7FFFFFFF) return FS4_ERR_SHAPE;
+      t.prefix[kind][i + 1] = (int32_t)acc;
+    }
   }
-  if (!fill_prefix(p, [](const MuonMat& m) { return m.m > kMuonThin ? (int64_t)(m.mp / 128) * (m.np / 64) : 0; })) return FS4_ERR_SHAPE;
-  if (!p.prefix[count]) return FS4_OK;
-  if (launch_muon_prepare(p, st, sms) != cudaSuccess) return FS4_ERR_CUDA;
-  for (int32_t k = 0; k < K; ++k) {
-    const float* c = coeffs + (n_coeffs == 1 ? 0 : 3 * k);
-    p.a = c[0]; p.b = c[1]; p.c = c[2];
-    p.slot = k & 1;
-    p.last = k == K - 1;
-    if (!fill_prefix(p, [](const MuonMat& m) { const int64_t T = m.m > kMuonThin ? m.mp / 256 : 0; return T * (T + 1) / 2; })) return FS4_ERR_SHAPE;
-    if (launch_muon_product(MuonProduct::GramX, p, st, sms) != cudaSuccess) return FS4_ERR_CUDA;
-    if (launch_muon_product(MuonProduct::GramA, p, st, sms) != cudaSuccess) return FS4_ERR_CUDA;
-    if (!fill_prefix(p, [](const MuonMat& m) { return m.m > kMuonThin ? (int64_t)(m.mp / 256) * (m.np / 256) : 0; })) return FS4_ERR_SHAPE;
-    if (launch_muon_product(MuonProduct::Update, p, st, sms) != cudaSuccess) return FS4_ERR_CUDA;
+  MuonCall c{};
+  c.ws = static_cast<uint8_t*>(workspace);
+  c.count = count;
+  c.K = K;
+  c.n_coeffs = n_coeffs;
+  c.nesterov = (flags & FS4_MUON_NESTEROV) ? 1 : 0;
+  c.beta = (float)beta;
+  c.rest = (float)(1.0 - beta);
+  c.rate = step ? (float)lr : -1.0f;
+  c.keep = step ? (float)(1.0 - lr * weight_decay) : 0.0f;
+  std::memcpy(c.coeffs, coeffs, sizeof(float) * 3 * n_coeffs);
+  if (launch_muon_moment(c, t, st) != cudaSuccess) return FS4_ERR_CUDA;
+  if (t.prefix[kUnitsThin][count] && launch_muon_thin(c, t.prefix[kUnitsThin][count], st) != cudaSuccess) return FS4_ERR_CUDA;
+  if (t.prefix[kUnitsPrepare][count]) {
+    if (launch_muon_prepare(c, t.prefix[kUnitsPrepare][count], st, sms) != cudaSuccess) return FS4_ERR_CUDA;
+    if (launch_muon_iterate(c, need, t.prefix[kUnitsGram][count], t.prefix[kUnitsUpdate][count], st) != cudaSuccess) return FS4_ERR_CUDA;
   }
   return FS4_OK;
 }

@@ -7,7 +7,8 @@
 // The norm is a sum of float64 partials in a fixed order (no atomics), so a step repeats bit
 // for bit.  A matrix whose norm is not finite gets X_0 = 0 and sets the status word: its
 // update is zero.  Both kernels are bound by HBM: moment reads G and M and writes M, prepare
-// reads them again and writes 4 bytes an element.
+// reads them again and writes 4 bytes an element.  Loads of four 8-element pieces are issued
+// before the first is used.
 #include <cstdint>
 
 #include "muon_device.cuh"
@@ -16,6 +17,7 @@ namespace fs4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 4;      // 8-element pieces in flight a thread
 
 __device__ __forceinline__ double block_sum(double v, double* red) {
 #pragma unroll
@@ -29,133 +31,192 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return s;
 }
 
-// Unit u of a matrix: `rows` whole rows of G, about kMuonUnit elements.
-__global__ void __launch_bounds__(kThreads) muon_moment_kernel(const __grid_constant__ MuonParams p) {
+// Unit u of a matrix: whole rows of G.  CTA 0 also leaves the table
+// in the workspace and resets the status word and the iterate kernel's barrier.
+template <int N>
+__global__ void __launch_bounds__(kThreads) muon_moment_kernel(const __grid_constant__ MuonCall p,
+                                                               const __grid_constant__ MuonTableN<N> t) {
   __shared__ double red[kThreads / 32];
+  if (blockIdx.x == 0) {
+    MuonTable* out = muon_table(p.ws);
+    for (int i = threadIdx.x; i < kUnitKinds * (p.count + 1); i += kThreads)
+      out->prefix[i / (p.count + 1)][i % (p.count + 1)] = t.prefix[i / (p.count + 1)][i % (p.count + 1)];
+    for (int i = threadIdx.x; i < p.count; i += kThreads) out->mat[i] = t.mat[i];
+    if (threadIdx.x == 0) {
+      *muon_status(p.ws) = 0u;
+      *muon_barrier(p.ws) = 0u;
+    }
+  }
   const int32_t u = blockIdx.x;
-  const MuonMat& d = p.mat[owner_of(p.prefix, p.count, u)];
-  const int32_t part = u - p.prefix[owner_of(p.prefix, p.count, u)];
-  const int64_t grows = d.tall ? d.n : d.m, gcols = d.tall ? d.m : d.n;
-  const int64_t per = (grows + d.parts - 1) / d.parts;
-  const int64_t r0 = part * per, r1 = r0 + per < grows ? r0 + per : grows;
+  if (u >= t.prefix[kUnitsMoment][p.count]) return;
+  const int mi = owner_of(t.prefix[kUnitsMoment], p.count, u);
+  const MuonMat& d = t.mat[mi];
+  const int32_t part = u - t.prefix[kUnitsMoment][mi];
+  const int32_t grows = d.tall ? d.n : d.m, gcols = d.tall ? d.m : d.n;
+  const int32_t per = (grows + d.parts - 1) / d.parts;
+  const int32_t r0 = part * per, r1 = min(r0 + per, grows);
   const bool vec = gcols % 8 == 0 && aligned16(d.g, d.ldg, d.tg) && (!d.mom || aligned16(d.mom, d.ldm, d.tm));
   double sum = 0.0;
-  if (r0 < r1) {
-    const int64_t width = vec ? gcols / 8 : gcols, count = (r1 - r0) * width;
-    for (int64_t i = threadIdx.x; i < count; i += kThreads) {
-      const int64_t r = r0 + i / width, c = i % width;
-      if (vec) {
-        float g[8], m[8];
-        get8(d.g, r * d.ldg + 8 * c, d.tg, g);
-        if (d.mom) {
-          get8(d.mom, r * d.ldm + 8 * c, d.tm, m);
+  if (vec) {
+    const int32_t width = gcols / 8, count = (r1 - r0) * width;
+    for (int32_t i0 = threadIdx.x; i0 < count; i0 += kAhead * kThreads) {
+      float g[kAhead][8], m[kAhead][8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) m[k] = fmaf(p.beta, m[k], p.rest * g[k]);
-          put8(d.mom, r * d.ldm + 8 * c, d.tm, m);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) g[k] = direction(p, m[k], g[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum += (double)g[k] * (double)g[k];
-      } else {
-        float g = get1(d.g, r * d.ldg + c, d.tg);
-        if (d.mom) {
-          const float m = put1(d.mom, r * d.ldm + c, d.tm,
-                              fmaf(p.beta, get1(d.mom, r * d.ldm + c, d.tm), p.rest * g));
-          g = direction(p, m, g);
-        }
-        sum += (double)g * (double)g;
+      for (int s = 0; s < kAhead; ++s) {
+        const int32_t i = i0 + s * kThreads;
+        if (i >= count) break;
+        const int64_t r = r0 + i / width, c = 8 * (i % width);
+        get8(d.g, r * d.ldg + c, d.tg, g[s]);
+        if (d.mom) get8(d.mom, r * d.ldm + c, d.tm, m[s]);
       }
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        const int32_t i = i0 + s * kThreads;
+        if (i >= count) break;
+        if (d.mom) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) m[s][k] = fmaf(p.beta, m[s][k], p.rest * g[s][k]);
+          put8(d.mom, (int64_t)(r0 + i / width) * d.ldm + 8 * (i % width), d.tm, m[s]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) g[s][k] = direction(p, m[s][k], g[s][k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += (double)g[s][k] * (double)g[s][k];
+      }
+    }
+  } else {
+    const int32_t count = (r1 - r0) * gcols;
+    for (int32_t i = threadIdx.x; i < count; i += kThreads) {
+      const int64_t r = r0 + i / gcols, c = i % gcols;
+      float g = get1(d.g, r * d.ldg + c, d.tg);
+      if (d.mom) {
+        const float m = put1(d.mom, r * d.ldm + c, d.tm, fmaf(p.beta, get1(d.mom, r * d.ldm + c, d.tm), p.rest * g));
+        g = direction(p, m, g);
+      }
+      sum += (double)g * (double)g;
     }
   }
   const double s = block_sum(sum, red);
-  if (threadIdx.x == 0) p.partials[d.partial + part] = s;
+  if (threadIdx.x == 0) muon_partials(p.ws)[d.partial + part] = s;
 }
 
-// Persistent; one 128 x 64 tile of X_0 at a time.
-__global__ void __launch_bounds__(kThreads) muon_prepare_kernel(const __grid_constant__ MuonParams p) {
+// Eight elements of U from (r, c) of G on; absent ones are 0.
+__device__ __forceinline__ void direction8(const MuonCall& p, const MuonMat& d, bool vec, int64_t r, int64_t c, int64_t rows,
+                                           int64_t cols, float* x) {
+  if (vec && r < rows && c + 8 <= cols) {
+    get8(d.g, r * d.ldg + c, d.tg, x);
+    if (d.mom) {
+      float m[8];
+      get8(d.mom, r * d.ldm + c, d.tm, m);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = direction(p, m[k], x[k]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = (r < rows && c + k < cols) ? direction_at(p, d, r, c + k) : 0.0f;
+  }
+}
+
+// Persistent, a contiguous range of 128 x 64 tiles of X_0 a CTA.  A tall matrix's tile turns in
+// shared memory: element (c, r) of G at word r ^ 4 (c / 8 % 8) of row c, so that the reads of
+// eight c at one r take different banks.
+__global__ void __launch_bounds__(kThreads) muon_prepare_kernel(const __grid_constant__ MuonCall p) {
   __shared__ double red[kThreads / 32];
-  __shared__ float turn[64][129];
-  const int32_t total = p.prefix[p.count];
+  __shared__ __align__(16) float turn[64 * 128];
+  const MuonTable& t = *muon_table(p.ws);
+  const int32_t* prefix = t.prefix[kUnitsPrepare];
+  const int32_t total = prefix[p.count];
   const int32_t per = (total + gridDim.x - 1) / gridDim.x;
   int32_t u = blockIdx.x * per;
-  const int32_t end = u + per < total ? u + per : total;
-  int cur = -1;
+  const int32_t end = min(u + per, total);
+  if (u >= end) return;
+  int mi = owner_of(prefix, p.count, u) - 1;
+  MuonMat d{};
   float inv = 0.0f;
+  int32_t next = u;
   for (; u < end; ++u) {
-    const int mi = owner_of(p.prefix, p.count, u);
-    const MuonMat& d = p.mat[mi];
-    if (mi != cur) {
-      cur = mi;
+    if (u == next) {      // the next matrix (those without tiles here have empty ranges)
+      do ++mi; while (prefix[mi + 1] <= u);
+      next = prefix[mi + 1];
+      d = t.mat[mi];
+      const double* part = muon_partials(p.ws) + d.partial;
       double s = 0.0;
-      for (int i = threadIdx.x; i < d.parts; i += kThreads) s += p.partials[d.partial + i];
+      for (int i = threadIdx.x; i < d.parts; i += kThreads) s += part[i];
       s = block_sum(s, red);
       const bool fine = isfinite(s);
-      inv = fine ? (float)(1.0 / (sqrt(s) + 1e-7)) * kXScale : 0.0f;
-      if (!fine && threadIdx.x == 0) atomicOr(p.status, kStatusNonFinite);
-      if (!fine) inv = -1.0f;      // the matrix is carried as zeros
+      inv = fine ? (float)(1.0 / (sqrt(s) + 1e-7)) * kXScale : -1.0f;   // -1: carried as zeros
+      if (!fine && threadIdx.x == 0) atomicOr(muon_status(p.ws), kStatusNonFinite);
     }
-    const int32_t t = u - p.prefix[mi], across = d.np / 64;
-    const int64_t r0 = (int64_t)(t / across) * 128, c0 = (int64_t)(t % across) * 64;
+    const int32_t tu = u - prefix[mi], across = d.np / 64;
+    const int64_t r0 = (int64_t)(tu / across) * 128, c0 = (int64_t)(tu % across) * 64;
     const MuonLayout L = muon_layout(d.mp, d.np);
     uint8_t* hi = p.ws + d.base + L.x[0];
     uint8_t* lo = p.ws + d.base + L.xl;
-    const bool vec = !d.tall && aligned16(d.g, d.ldg, d.tg) && (!d.mom || aligned16(d.mom, d.ldm, d.tm));
+    const bool vec = aligned16(d.g, d.ldg, d.tg) && (!d.mom || aligned16(d.mom, d.ldm, d.tm));
+    float x[kAhead][8];
     if (d.tall) {
-      __syncthreads();
-      // G is n x m: its rows c0.. and columns r0.. land transposed
-      for (int i = threadIdx.x; i < 64 * 128; i += kThreads) {
-        const int64_t c = c0 + (i >> 7), r = r0 + (i & 127);
-        turn[i >> 7][i & 127] = (c < d.n && r < d.m) ? direction_at(p, d, c, r) : 0.0f;
+      // G is n x m: rows c0 .., columns r0 ..
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        const int q = threadIdx.x + s * kThreads;      // 64 rows x 16 pieces
+        direction8(p, d, vec, c0 + (q >> 4), r0 + 8 * (q & 15), d.n, d.m, x[s]);
       }
       __syncthreads();
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        const int q = threadIdx.x + s * kThreads, c = q >> 4, r = 8 * (q & 15), sw = 4 * ((c >> 3) & 7);
+        *reinterpret_cast<float4*>(turn + 128 * c + (r ^ sw)) = make_float4(x[s][0], x[s][1], x[s][2], x[s][3]);
+        *reinterpret_cast<float4*>(turn + 128 * c + ((r + 4) ^ sw)) = make_float4(x[s][4], x[s][5], x[s][6], x[s][7]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        const int q = threadIdx.x + s * kThreads, r = q >> 3, c = 8 * (q & 7);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[s][k] = turn[128 * (c + k) + (r ^ (4 * (q & 7)))];
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        const int q = threadIdx.x + s * kThreads;      // 128 rows x 8 pieces
+        direction8(p, d, vec, r0 + (q >> 3), c0 + 8 * (q & 7), d.m, d.n, x[s]);
+      }
     }
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int q = threadIdx.x + s * kThreads;        // 128 rows x 8 chunks
-      const int64_t r = r0 + (q >> 3), c = c0 + 8 * (q & 7);
-      float x[8];
-      if (d.tall) {
+    for (int s = 0; s < kAhead; ++s) {
+      const int q = threadIdx.x + s * kThreads;
+      float y[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = turn[8 * (q & 7) + k][q >> 3];
-      } else if (vec && r < d.m && c + 8 <= d.n) {
-        get8(d.g, r * d.ldg + c, d.tg, x);
-        if (d.mom) {
-          float m[8];
-          get8(d.mom, r * d.ldm + c, d.tm, m);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = direction(p, m[k], x[k]);
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = (r < d.m && c + k < d.n) ? direction_at(p, d, r, c + k) : 0.0f;
-      }
-      uint32_t h[4], l[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float a = inv < 0.0f ? 0.0f : x[2 * k] * inv, b = inv < 0.0f ? 0.0f : x[2 * k + 1] * inv;
-        const __half2 hh = __floats2half2_rn(a, b);
-        h[k] = *reinterpret_cast<const uint32_t*>(&hh);
-        const __half2 ll = __floats2half2_rn((a - half_lo(h[k])) * kLowScale, (b - half_hi(h[k])) * kLowScale);
-        l[k] = *reinterpret_cast<const uint32_t*>(&ll);
-      }
-      const int64_t off = tiled_chunk_offset_bf16(r, c, d.np);
-      *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+      for (int k = 0; k < 8; ++k) y[k] = inv < 0.0f ? 0.0f : x[s][k] * inv;
+      uint4 h, l;
+      split8(y, h, l);
+      const int64_t off = tiled_chunk_offset_bf16(r0 + (q >> 3), c0 + 8 * (q & 7), d.np);
+      *reinterpret_cast<uint4*>(hi + off) = h;
+      *reinterpret_cast<uint4*>(lo + off) = l;
     }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_muon_moment(const MuonParams& p, cudaStream_t st, int num_sms) {
-  muon_moment_kernel<<<(unsigned)p.prefix[p.count], kThreads, 0, st>>>(p);
+cudaError_t launch_muon_moment(const MuonCall& c, const MuonTable& t, cudaStream_t st) {
+  const int32_t units = t.prefix[kUnitsMoment][c.count];
+  const unsigned grid = (unsigned)(units > 0 ? units : 1);
+  if (c.count <= kMuonFew) {
+    MuonTableN<kMuonFew> few;
+    for (int k = 0; k < kUnitKinds; ++k)
+      for (int i = 0; i <= kMuonFew; ++i) few.prefix[k][i] = t.prefix[k][i < c.count ? i : c.count];
+    for (int i = 0; i < kMuonFew; ++i) few.mat[i] = t.mat[i < c.count ? i : 0];
+    muon_moment_kernel<kMuonFew><<<grid, kThreads, 0, st>>>(c, few);
+  } else {
+    muon_moment_kernel<kMuonMaxBatch><<<grid, kThreads, 0, st>>>(c, t);
+  }
   return cudaGetLastError();
 }
 
-cudaError_t launch_muon_prepare(const MuonParams& p, cudaStream_t st, int num_sms) {
-  const int total = p.prefix[p.count], most = 4 * num_sms;
-  muon_prepare_kernel<<<(unsigned)(total < most ? total : most), kThreads, 0, st>>>(p);
+cudaError_t launch_muon_prepare(const MuonCall& c, int32_t units, cudaStream_t st, int num_sms) {
+  const int most = 4 * num_sms;
+  muon_prepare_kernel<<<(unsigned)(units < most ? units : most), kThreads, 0, st>>>(c);
   return cudaGetLastError();
 }
 

@@ -89,14 +89,39 @@ __device__ __forceinline__ void put8(void* p, int64_t i, int type, float* v) {
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-__device__ __forceinline__ float direction(const MuonParams& p, float mom, float g) {
+__device__ __forceinline__ float direction(const MuonCall& p, float mom, float g) {
   return p.nesterov ? fmaf(p.beta, mom, p.rest * g) : mom;
 }
 
 // Update direction at (r, c) of G.
-__device__ __forceinline__ float direction_at(const MuonParams& p, const MuonMat& d, int64_t r, int64_t c) {
+__device__ __forceinline__ float direction_at(const MuonCall& p, const MuonMat& d, int64_t r, int64_t c) {
   const float g = get1(d.g, r * d.ldg + c, d.tg);
   return d.mom ? direction(p, get1(d.mom, r * d.ldm + c, d.tm), g) : g;
+}
+
+// FP16 parts of eight values: value = high + low, to 22 significand bits or 2^-25, whichever is
+// more (values are scaled: X by 2^12, A by 2^8).
+__device__ __forceinline__ uint32_t two_halves(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void join8(uint4 hi, uint4 lo, float* v) {
+  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = half_lo(l[i]) + half_lo(h[i]);
+    v[2 * i + 1] = half_hi(l[i]) + half_hi(h[i]);
+  }
+}
+__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = two_halves(v[2 * i], v[2 * i + 1]);
+    l[i] = two_halves(v[2 * i] - half_lo(h[i]), v[2 * i + 1] - half_hi(h[i]));
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 }  // namespace fs4

@@ -9,18 +9,19 @@
 
 namespace fs4 {
 
-constexpr int kMuonMaxBatch = 224;      // matrices per call (kernel-parameter table size)
-constexpr int64_t kMuonHeader = 256;    // byte 0 of the workspace: the status word
+constexpr int kMuonMaxBatch = 224;      // matrices per call
+constexpr int kMuonFew = 8;             // calls of at most this many pass a small parameter block
 constexpr int kMuonPad = 256;           // working dimensions are padded to multiples of 256
-constexpr int64_t kMuonUnit = 16384;    // elements of one partial sum of squares, about
+constexpr int64_t kMuonUnit = 4096;     // least elements of one partial sum of squares
+constexpr int64_t kMuonParts = 1184;    // about the most partial sums of a matrix (8 CTAs an SM)
 
 // Matrices with at most this many rows (working orientation) take the thin kernels (muon_thin.cu).
 constexpr int kMuonThin = 32;
 constexpr int kMuonChunk = 256;         // columns of one unit of the thin kernels
 
-// FP16 operands hold value * 2^k, and a low part holds what the high part lost * 2^11 more:
-// X has elements of at most about 1.2 and of 1 / sqrt(n) typically, A and B of a few units.
-constexpr float kXScale = 4096.0f, kAScale = 256.0f, kLowScale = 2048.0f;
+// FP16 operands hold value * 2^k: X has elements of at most about 1.2 and of 1 / sqrt(n)
+// typically, A and B of a few units.
+constexpr float kXScale = 4096.0f, kAScale = 256.0f;
 
 // One matrix.  The working X is G or, for a tall G, G^T: m x n with m <= n.
 struct MuonMat {
@@ -36,6 +37,38 @@ struct MuonMat {
   int8_t tg, tm, tw, pad;  // element types
   float scale;             // the update is scale * X_K
 };
+
+// Work units of each kernel and matrix, as prefix sums.
+enum MuonUnits { kUnitsMoment = 0, kUnitsThin, kUnitsPrepare, kUnitsGram, kUnitsUpdate, kUnitKinds };
+
+template <int N>
+struct MuonTableN {
+  int32_t prefix[kUnitKinds][N + 1];
+  MuonMat mat[N];
+};
+// The first kernel of a call gets the table as a parameter and leaves a copy in the workspace for
+// the others: a 25 KB parameter block costs each launch about 10 us of host time.
+using MuonTable = MuonTableN<kMuonMaxBatch>;
+
+// What every kernel of a call needs.
+struct MuonCall {
+  uint8_t* ws;
+  int32_t count;
+  int32_t K, n_coeffs;
+  int32_t nesterov;
+  float beta, rest;        // momentum and 1 - momentum
+  float keep, rate;        // weights <- keep * weights - rate * scale * X_K; rate < 0: output = scale * X_K
+  float coeffs[3 * FS4_MAX_ITERS];
+};
+
+// Workspace: [header | table | partial sums | one block per matrix].  Header: the status word at
+// byte 0, the iterate kernel's barrier count at byte 128.
+constexpr int64_t kMuonHeader = 256, kMuonBarrier = 128;
+constexpr int64_t kMuonPartials = (kMuonHeader + (int64_t)sizeof(MuonTable) + 255) / 256 * 256;
+__host__ __device__ inline uint32_t* muon_status(uint8_t* ws) { return reinterpret_cast<uint32_t*>(ws); }
+__host__ __device__ inline uint32_t* muon_barrier(uint8_t* ws) { return reinterpret_cast<uint32_t*>(ws + kMuonBarrier); }
+__host__ __device__ inline MuonTable* muon_table(uint8_t* ws) { return reinterpret_cast<MuonTable*>(ws + kMuonHeader); }
+__host__ __device__ inline double* muon_partials(uint8_t* ws) { return reinterpret_cast<double*>(ws + kMuonPartials); }
 
 // Byte offsets inside a matrix's block: X high parts (two, by iteration parity) and low part,
 // A high and low, B, then the diagonals of A and B (FP32).  Matrices in the TILED BF16 layout
@@ -65,32 +98,10 @@ __host__ __device__ inline int64_t thin_gram_offset(int64_t m) { return (4 * m *
 __host__ __device__ inline int64_t thin_chunks(int64_t n) { return (n + kMuonChunk - 1) / kMuonChunk; }
 __host__ __device__ inline int64_t thin_bytes(int64_t m, int64_t n) { return thin_gram_offset(m) + 8 * m * m * thin_chunks(n); }
 
-struct MuonParams {
-  int32_t count;
-  int32_t slot;            // X's current high part
-  int32_t last;            // the last update: write the weights or the output
-  int32_t nesterov;
-  float a, b, c;           // this iteration's polynomial
-  float beta, rest;        // momentum and 1 - momentum
-  float keep, rate;        // weights <- keep * weights - rate * scale * X_K; rate < 0: output = scale * X_K
-  uint32_t* status;
-  double* partials;
-  uint8_t* ws;
-  int32_t prefix[kMuonMaxBatch + 1];
-  MuonMat mat[kMuonMaxBatch];
-};
-static_assert(sizeof(MuonParams) <= 32000, "kernel parameter block too large");
-
-enum class MuonProduct : int { GramX = 0, GramA = 1, Update = 2 };
-
-cudaError_t launch_muon_moment(const MuonParams& p, cudaStream_t st, int num_sms);
-cudaError_t launch_muon_prepare(const MuonParams& p, cudaStream_t st, int num_sms);
-// Thin matrices: Gram matrices, the iteration on them (coeffs: K or one triple), the result.
-struct MuonCoeffs {
-  int32_t K, n;
-  float v[3 * FS4_MAX_ITERS];
-};
-cudaError_t launch_muon_thin(const MuonParams& p, const MuonCoeffs& c, cudaStream_t st);
-cudaError_t launch_muon_product(MuonProduct e, const MuonParams& p, cudaStream_t st, int num_sms);
+// launchers; the unit counts come from the table's prefix sums
+cudaError_t launch_muon_moment(const MuonCall& c, const MuonTable& t, cudaStream_t st);
+cudaError_t launch_muon_thin(const MuonCall& c, int32_t units, cudaStream_t st);
+cudaError_t launch_muon_prepare(const MuonCall& c, int32_t units, cudaStream_t st, int num_sms);
+cudaError_t launch_muon_iterate(const MuonCall& c, int64_t ws_bytes, int32_t gram_units, int32_t update_units, cudaStream_t st);
 
 }  // namespace fs4

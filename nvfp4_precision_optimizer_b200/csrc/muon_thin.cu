@@ -21,7 +21,7 @@ constexpr int kThreads = 256;
 static_assert(kMuonChunk == kThreads, "one column a thread");
 
 // U's columns c0 .. c0 + 255 into u[row][column].
-__device__ __forceinline__ void load_chunk(const MuonParams& p, const MuonMat& d, int64_t c0, float (*u)[kMuonChunk + 1]) {
+__device__ __forceinline__ void load_chunk(const MuonCall& p, const MuonMat& d, int64_t c0, float (*u)[kMuonChunk + 1]) {
   const int count = d.m * kMuonChunk;
   for (int i = threadIdx.x; i < count; i += kThreads) {
     // neighbouring threads read neighbouring elements of G
@@ -32,11 +32,12 @@ __device__ __forceinline__ void load_chunk(const MuonParams& p, const MuonMat& d
   }
 }
 
-__global__ void __launch_bounds__(kThreads) muon_thin_gram_kernel(const __grid_constant__ MuonParams p) {
+__global__ void __launch_bounds__(kThreads) muon_thin_gram_kernel(const __grid_constant__ MuonCall p) {
   __shared__ float u[kMuonThin][kMuonChunk + 1];
-  const int mi = owner_of(p.prefix, p.count, blockIdx.x);
-  const MuonMat& d = p.mat[mi];
-  const int32_t chunk = blockIdx.x - p.prefix[mi];
+  const MuonTable& t = *muon_table(p.ws);
+  const int mi = owner_of(t.prefix[kUnitsThin], p.count, blockIdx.x);
+  const MuonMat& d = t.mat[mi];
+  const int32_t chunk = blockIdx.x - t.prefix[kUnitsThin][mi];
   load_chunk(p, d, (int64_t)chunk * kMuonChunk, u);
   __syncthreads();
   double* out = reinterpret_cast<double*>(p.ws + d.base + thin_gram_offset(d.m)) + (int64_t)chunk * d.m * d.m;
@@ -48,10 +49,9 @@ __global__ void __launch_bounds__(kThreads) muon_thin_gram_kernel(const __grid_c
   }
 }
 
-__global__ void __launch_bounds__(1024) muon_thin_iterate_kernel(const __grid_constant__ MuonParams p,
-                                                                 const __grid_constant__ MuonCoeffs k) {
+__global__ void __launch_bounds__(1024) muon_thin_iterate_kernel(const __grid_constant__ MuonCall p) {
   __shared__ double A[kMuonThin][kMuonThin + 1], S[kMuonThin][kMuonThin + 1], T[kMuonThin][kMuonThin + 1], W[kMuonThin][kMuonThin + 1];
-  const MuonMat& d = p.mat[blockIdx.x];
+  const MuonMat& d = muon_table(p.ws)->mat[blockIdx.x];
   const int m = d.m;
   if (m > kMuonThin) return;
   uint8_t* ws = p.ws + d.base;
@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(1024) muon_thin_iterate_kernel(const __grid_co
     for (int t = 0; t < m; ++t) s += x[i][t] * y[t][j];
     return s;
   };
-  for (int it = 0; it < k.K; ++it) {
-    const float* c = k.v + (k.n == 1 ? 0 : 3 * it);
+  for (int it = 0; it < p.K; ++it) {
+    const float* c = p.coeffs + (p.n_coeffs == 1 ? 0 : 3 * it);
     if (mine) S[i][j] = (double)c[1] * A[i][j] + (double)c[2] * dot(A, A) + (i == j ? (double)c[0] : 0.0);
     __syncthreads();
     double t = 0.0;
@@ -100,16 +100,17 @@ __global__ void __launch_bounds__(1024) muon_thin_iterate_kernel(const __grid_co
   if (mine) reinterpret_cast<float*>(ws)[threadIdx.x] = fine ? (float)T[i][j] : 0.0f;
   if (threadIdx.x == 0) {
     *reinterpret_cast<float*>(ws + thin_flag_offset(m)) = fine ? 1.0f : 0.0f;
-    if (!fine) atomicOr(p.status, kStatusNonFinite);
+    if (!fine) atomicOr(muon_status(p.ws), kStatusNonFinite);
   }
 }
 
-__global__ void __launch_bounds__(kThreads) muon_thin_apply_kernel(const __grid_constant__ MuonParams p) {
+__global__ void __launch_bounds__(kThreads) muon_thin_apply_kernel(const __grid_constant__ MuonCall p) {
   __shared__ float u[kMuonThin][kMuonChunk + 1];
   __shared__ float T[kMuonThin][kMuonThin];
-  const int mi = owner_of(p.prefix, p.count, blockIdx.x);
-  const MuonMat& d = p.mat[mi];
-  const int64_t c0 = (int64_t)(blockIdx.x - p.prefix[mi]) * kMuonChunk;
+  const MuonTable& t = *muon_table(p.ws);
+  const int mi = owner_of(t.prefix[kUnitsThin], p.count, blockIdx.x);
+  const MuonMat& d = t.mat[mi];
+  const int64_t c0 = (int64_t)(blockIdx.x - t.prefix[kUnitsThin][mi]) * kMuonChunk;
   const uint8_t* ws = p.ws + d.base;
   const bool fine = *reinterpret_cast<const float*>(ws + thin_flag_offset(d.m)) != 0.0f;
   for (int e = threadIdx.x; e < d.m * d.m; e += kThreads) T[e / d.m][e % d.m] = reinterpret_cast<const float*>(ws)[e];
@@ -137,16 +138,15 @@ __global__ void __launch_bounds__(kThreads) muon_thin_apply_kernel(const __grid_
     const int64_t at = d.tall ? (c0 + c) * d.ldw + r : r * d.ldw + c0 + c;
     put1(d.w, at, d.tw, p.rate < 0.0f ? v : fmaf(-p.rate, v, p.keep * get1(d.w, at, d.tw)));
   }
-  if (bad) atomicOr(p.status, kStatusNonFinite);
+  if (bad) atomicOr(muon_status(p.ws), kStatusNonFinite);
 }
 
 }  // namespace
 
-cudaError_t launch_muon_thin(const MuonParams& p, const MuonCoeffs& c, cudaStream_t st) {
-  const unsigned units = (unsigned)p.prefix[p.count];
-  muon_thin_gram_kernel<<<units, kThreads, 0, st>>>(p);
-  muon_thin_iterate_kernel<<<(unsigned)p.count, kMuonThin * kMuonThin, 0, st>>>(p, c);
-  muon_thin_apply_kernel<<<units, kThreads, 0, st>>>(p);
+cudaError_t launch_muon_thin(const MuonCall& c, int32_t units, cudaStream_t st) {
+  muon_thin_gram_kernel<<<(unsigned)units, kThreads, 0, st>>>(c);
+  muon_thin_iterate_kernel<<<(unsigned)c.count, kMuonThin * kMuonThin, 0, st>>>(c);
+  muon_thin_apply_kernel<<<(unsigned)units, kThreads, 0, st>>>(c);
   return cudaGetLastError();
 }
 

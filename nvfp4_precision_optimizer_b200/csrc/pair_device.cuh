@@ -2,6 +2,8 @@
 // 256-row tensor-core tile over two SMs, each SM holding half of either operand.
 #pragma once
 
+#include <cuda.h>
+
 #include "mx_device.cuh"
 
 namespace fs4 {
@@ -32,9 +34,22 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
-// Arrive on a barrier given by its cluster address (cluster_map).
+// Arrive on a barrier given by its cluster address (cluster_map).  A release at cluster scope
+// costs about 1200 cycles: once a tile, not once a stage.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// Copy of `rows` (the map's box) 128-byte rows from row `row` on to this CTA's shared memory; the
+// bytes are counted on `bar`, a cluster address in either CTA of the pair.  x is always 0.
+__device__ __forceinline__ void tma_rows_pair(uint32_t dst, const CUtensorMap* map, int32_t row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(0), "r"(row)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {

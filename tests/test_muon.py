@@ -86,9 +86,10 @@ def test_workspace_sizes(F):
     assert F.muon_workspace_size([(0, 4)]) == 0 and F.muon_workspace_size([(4, 65537)]) == 0
     assert F.muon_workspace_size([(16, 16)] * 225) == 0
     a, b = F.muon_workspace_size([(300, 1000)]), F.muon_workspace_size([(1000, 300)])
-    # X in three FP16 parts, A in two and B in one, and two diagonals, on sizes padded to 256
+    # X in three FP16 parts, A in two and B in one, and two diagonals, on sizes padded to 256,
+    # beside the table of matrices and the partial sums
     floor = 6 * 512 * 1024 + 6 * 512 * 512 + 8 * 512
-    assert floor < a <= floor + 4096 and floor < b <= floor + 4096
+    assert floor < a <= floor + (1 << 16) and floor < b <= floor + (1 << 16)
 
 
 def test_binding_refusals(F):
