@@ -12,7 +12,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libfs4.so")
 SOURCES = ["kernels.cu", "gemm.cu", "momentum.cu", "api.cu", "noalloc.cu",
-           "mxfp4.cu", "mxfp4_gemm.cu", "api_mx.cu",
+           "mxfp4.cu", "mxfp4_gemm.cu", "mxfp4_pair.cu", "api_mx.cu",
            "muon.cu", "muon_iterate.cu", "muon_thin.cu", "api_muon.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -129,24 +129,6 @@ __device__ __forceinline__ void load_columns(const Maps& m, uint32_t dst, int64_
 }
 
 // ------------------------------------------------------------------ epilogue
-// 32 bytes = two 16-byte chunks of a tile row.  Loads bypass L1: other SMs wrote the data
-// earlier in this launch.
-struct Pair {
-  uint32_t w[8];
-};
-__device__ __forceinline__ Pair load_pair(const uint8_t* p) {
-  Pair r;
-  asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
-               : "l"(p)
-               : "memory");
-  return r;
-}
-__device__ __forceinline__ void store_pair(void* p, const Pair& r) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3]),
-               "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
-               : "memory");
-}
 // Chunks 2 i and 2 i + 1 of a row lie in one 32-byte piece, in the order of the row's bit 0.
 __device__ __forceinline__ Pair ordered(const Pair& r, bool swap) {
   Pair o;
@@ -158,13 +140,6 @@ __device__ __forceinline__ Pair ordered(const Pair& r, bool swap) {
   return o;
 }
 __device__ __forceinline__ uint4 quad(const Pair& p, int i) { return make_uint4(p.w[4 * i], p.w[4 * i + 1], p.w[4 * i + 2], p.w[4 * i + 3]); }
-
-__device__ __forceinline__ float get_as(const float* p) { return *p; }
-__device__ __forceinline__ float get_as(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float get_as(const __half* p) { return __half2float(*p); }
-__device__ __forceinline__ void put_as(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put_as(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put_as(__half* p, float v) { *p = __float2half_rn(v); }
 
 // 32 results (columns col .. col + 31 of working row `row`) into the weights or the output.
 template <typename T>
@@ -183,7 +158,7 @@ __device__ __forceinline__ void write_result(const MuonCall& p, const MuonMat& d
 #pragma unroll
     for (int q = 0; q < 32 / kPer; ++q) {
       Pair r{};
-      if (blend) r = load_pair(reinterpret_cast<const uint8_t*>(at + q * kPer));
+      if (blend) r = load_pair(at + q * kPer);
       T* e = reinterpret_cast<T*>(r.w);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -470,7 +445,7 @@ __device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, uint32_t& 
     __syncwarp();
     if (lane == 0) {
       if (rank == 0) mbar_arrive(&sh.acc_empty[b]);
-      else mbar_arrive_cluster(cluster_map(smem_addr(&sh.acc_empty[b]), 0));
+      else mbar_arrive_remote(cluster_map(smem_addr(&sh.acc_empty[b]), 0));
     }
   }
   return true;

@@ -36,6 +36,7 @@ struct MxGemmArgs {
   int32_t accumulate;
   uint32_t* status;
 };
+cudaError_t launch_mxfp4_pair(const MxGemmArgs& a, cudaStream_t st);   // mxfp4_pair.cu
 cudaError_t launch_mxfp4_gemm(const MxGemmArgs& a, cudaStream_t st, int num_sms);
 
 }  // namespace fs4

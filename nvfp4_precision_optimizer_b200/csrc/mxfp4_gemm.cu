@@ -225,6 +225,7 @@ cudaError_t launch_tile(const TileArgs& a, int64_t tiles, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_mxfp4_gemm(const MxGemmArgs& g, cudaStream_t st, int num_sms) {
+  if (((g.M + 255) / 256) * ((g.N + 255) / 256) >= 40) return launch_mxfp4_pair(g, st);
   TileArgs a{};
   // the narrow side: A's rows when they are at most 64 and no more than B's
   const bool swap = g.M <= 64 && g.M <= g.N;

@@ -34,10 +34,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
-// Arrive on a barrier given by its cluster address (cluster_map).  A release at cluster scope
-// costs about 1200 cycles: once a tile, not once a stage.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+// Arrive on a barrier given by its cluster address (cluster_map), to hand TMEM back: the tcgen05
+// fences order the accesses and no memory is published, so the release stays at the default
+// (CTA) scope.  At cluster scope it takes about 1200 cycles.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // Copy of `rows` (the map's box) 128-byte rows from row `row` on to this CTA's shared memory; the
@@ -96,5 +97,50 @@ __device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t next
   d |= (uint64_t)2 << 61;
   return d;
 }
+
+// MXFP4 operands: scale atoms to both CTAs' TMEM, each from its own shared memory ...
+__device__ __forceinline__ void tc_copy_sf_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+// ... the arrival of a thread's tcgen05 operations on one barrier of this CTA ...
+__device__ __forceinline__ void tc_commit_own(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// ... and the MMA of a CTA pair (K = 64).
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa_tmem,
+                                                 uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+
+// ------------------------------------------------------------------ 32-byte global accesses
+struct Pair {
+  uint32_t w[8];
+};
+// Loads bypass L1: the data may have been written by other SMs earlier in the launch.
+__device__ __forceinline__ Pair load_pair(const void* p) {
+  Pair r;
+  asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+               : "l"(p)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ void store_pair(void* p, const Pair& r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3]),
+               "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+               : "memory");
+}
+
+__device__ __forceinline__ float get_as(const float* p) { return *p; }
+__device__ __forceinline__ float get_as(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float get_as(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ void put_as(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put_as(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put_as(__half* p, float v) { *p = __float2half_rn(v); }
 
 }  // namespace fs4

@@ -113,7 +113,8 @@ def operand(fs4, rows, k, seed):
 
 
 PRODUCTS = [(1, 1, 1), (1, 16, 32), (1, 300, 700), (7, 129, 257), (16, 128, 2048), (17, 520, 300), (33, 65, 64), (64, 1000, 1536),
-            (65, 40, 515), (128, 128, 256), (130, 257, 1000), (300, 16, 2100), (513, 300, 130), (256, 512, 4096), (700, 1100, 96)]
+            (65, 40, 515), (128, 128, 256), (130, 257, 1000), (300, 16, 2100), (513, 300, 130), (256, 512, 4096), (700, 1100, 96),
+            (1790, 1300, 300), (513, 3600, 520), (4100, 1030, 130), (2048, 1280, 2048)]
 
 
 @pytest.mark.parametrize("kind", TYPES)
