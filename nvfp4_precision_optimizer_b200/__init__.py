@@ -7,7 +7,6 @@ streams) into those calls.  There is no CPU or fallback path.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Sequence
 
@@ -189,54 +188,70 @@ def _check_matrix(x: torch.Tensor, name: str, device: torch.device | None = None
 
 
 def _check_bytes(t: torch.Tensor, need: int, name: str, device: torch.device) -> None:
-    if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != device or t.numel() < need:
+    if t.dtype != torch.uint8 or t.device != device or t.numel() < need or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {need} bytes on {device}")
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream):
-    """Makes `device` and `stream` (default: the device's current one) current, so that what a
-    call allocates or zeroes belongs to the stream it runs on; yields the stream's handle."""
+def _on(device: torch.device, stream, body):
+    """body(stream handle) with `device` and `stream` (default: the device's current one) current,
+    so that what a call allocates or zeroes belongs to the stream it runs on."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return body(torch._C._cuda_getCurrentRawStream(device.index))
     if stream is not None and stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield torch.cuda.current_stream(device).cuda_stream
+        return body(torch.cuda.current_stream(device).cuda_stream)
 
 
 def mxfp4_tiled_shape(rows: int, cols: int) -> tuple[int, int]:
     """(codes bytes, scales bytes) of a rows x cols MXFP4 matrix in the TILED layout."""
-    rp, cp = _round_up(rows, 128), _round_up(cols, 256)
-    return rp * cp // 2, rp * cp // 32
+    padded = (rows + 127) // 128 * 128 * ((cols + 255) // 256 * 256)
+    return padded // 2, padded // 32
 
 
 def _mx_sizes(rows: int, cols: int, tiled: bool) -> tuple[int, int]:
     return mxfp4_tiled_shape(rows, cols) if tiled else (rows * ((cols + 1) // 2), rows * ((cols + 31) // 32))
 
 
+def _mx_check(op, rows: int, cols: int, tiled: bool, name: str, device) -> None:
+    """(codes, scales) of a rows x cols view."""
+    codes, scales = op
+    n_codes, n_scales = _mx_sizes(rows, cols, tiled)
+    _check_bytes(codes, n_codes, name, device)
+    _check_bytes(scales, n_scales, name, device)
+
+
 def _mx_view(rows: int, cols: int, tiled: bool, device, out):
-    need = _mx_sizes(rows, cols, tiled)
     if out is not None:
-        for t, n, name in zip(out, need, ("codes", "scales")):
-            _check_bytes(t, n, name, device)
+        _mx_check(out, rows, cols, tiled, "out", device)
         return out
-    shapes = [(n,) for n in need] if tiled else [(rows, (cols + 1) // 2), (rows, (cols + 31) // 32)]
-    return tuple(torch.empty(s, dtype=torch.uint8, device=device) for s in shapes)
+    if tiled:
+        a, b = mxfp4_tiled_shape(rows, cols)
+        return (torch.empty(a, dtype=torch.uint8, device=device), torch.empty(b, dtype=torch.uint8, device=device))
+    return (torch.empty((rows, (cols + 1) // 2), dtype=torch.uint8, device=device),
+            torch.empty((rows, (cols + 31) // 32), dtype=torch.uint8, device=device))
 
 
 def _mx_scale_flag(scale_rule: str) -> int:
-    if scale_rule not in ("floor", "ceil"):
+    if scale_rule == "floor":
+        return 0
+    if scale_rule != "ceil":
         raise ValueError(f"scale_rule must be 'floor' or 'ceil', not {scale_rule!r}")
-    return _lib.FS4_MX_SCALE_CEIL if scale_rule == "ceil" else 0
+    return _lib.FS4_MX_SCALE_CEIL
 
 
 def _mx_quantize(x, row, col, tiled, scale_rule, seed, handle):
     flags = _mx_scale_flag(scale_rule) | (FS4_LAYOUT_TILED if tiled else 0)
-    flags |= 0 if seed is None else _lib.FS4_MX_STOCHASTIC
+    if seed is None:
+        seed = 0
+    else:
+        flags |= _lib.FS4_MX_STOCHASTIC
+        seed = int(seed) & 0xFFFFFFFFFFFFFFFF
     rows, cols = x.shape
-    check(_lib.lib().fs4_mxfp4_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, cols, _ld(x),
-                                        *(_ptr(t) for t in (row or (None, None))),
-                                        *(_ptr(t) for t in (col or (None, None))), flags,
-                                        0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF, handle),
+    rc, rs = (None, None) if row is None else (row[0].data_ptr(), row[1].data_ptr())
+    cc, cs = (None, None) if col is None else (col[0].data_ptr(), col[1].data_ptr())
+    check(_lib.lib().fs4_mxfp4_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, cols, _ld(x), rc, rs, cc, cs, flags, seed,
+                                        handle),
           "fs4_mxfp4_quantize")
 
 
@@ -247,14 +262,21 @@ def mxfp4_quantize(x: torch.Tensor, axis: int = FS4_AXIS_ROW, tiled: bool = Fals
     saturates nothing; a seed rounds stochastically.  Returns (codes, scales); `out` is such
     a pair to write into."""
     _check_matrix(x, "x")
-    if axis not in (FS4_AXIS_ROW, FS4_AXIS_COL):
+    if axis != FS4_AXIS_ROW and axis != FS4_AXIS_COL:
         raise ValueError(f"axis must be FS4_AXIS_ROW or FS4_AXIS_COL, not {axis}")
-    rows, cols = x.shape if axis == FS4_AXIS_ROW else reversed(x.shape)
-    with _on(x.device, stream) as handle:
-        view = _mx_view(rows, cols, tiled, x.device, out)
-        row, col = (view, None) if axis == FS4_AXIS_ROW else (None, view)
-        _mx_quantize(x, row, col, tiled, scale_rule, seed, handle)
-    return view
+    dev = x.device
+
+    def body(handle):
+        rows, cols = x.shape
+        if axis == FS4_AXIS_ROW:
+            view = _mx_view(rows, cols, tiled, dev, out)
+            _mx_quantize(x, view, None, tiled, scale_rule, seed, handle)
+        else:
+            view = _mx_view(cols, rows, tiled, dev, out)
+            _mx_quantize(x, None, view, tiled, scale_rule, seed, handle)
+        return view
+
+    return _on(dev, stream, body)
 
 
 def mxfp4_quantize_both(x: torch.Tensor, tiled: bool = False, scale_rule: str = "floor", seed: int | None = None,
@@ -262,27 +284,26 @@ def mxfp4_quantize_both(x: torch.Tensor, tiled: bool = False, scale_rule: str = 
     """The row view and the column view of x in one pass over it (fs4_mxfp4_quantize), as a
     training step needs them.  Returns ((codes, scales) of x, (codes, scales) of x^T)."""
     _check_matrix(x, "x")
-    rows, cols = x.shape
-    with _on(x.device, stream) as handle:
-        row = _mx_view(rows, cols, tiled, x.device, None if out is None else out[0])
-        col = _mx_view(cols, rows, tiled, x.device, None if out is None else out[1])
+    dev = x.device
+
+    def body(handle):
+        rows, cols = x.shape
+        row = _mx_view(rows, cols, tiled, dev, None if out is None else out[0])
+        col = _mx_view(cols, rows, tiled, dev, None if out is None else out[1])
         _mx_quantize(x, row, col, tiled, scale_rule, seed, handle)
-    return row, col
+        return row, col
+
+    return _on(dev, stream, body)
 
 
-def _mx_check_operand(op, rows: int, cols: int, tiled: bool, name: str, device) -> None:
-    for t, need, part in zip(op, _mx_sizes(rows, cols, tiled), ("codes", "scales")):
-        _check_bytes(t, need, f"{name} {part}", device)
-
-
-def _mx_out(out, shape, dtype, device):
+def _mx_out(out, rows: int, cols: int, dtype, device):
     if out is None:
         if dtype not in _DTYPES:
             raise ValueError(f"dtype must be float32, bfloat16 or float16, not {dtype}")
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty((rows, cols), dtype=dtype, device=device)
     _check_matrix(out, "out", device)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"out must be {shape[0]} x {shape[1]}, got {tuple(out.shape)}")
+    if out.shape[0] != rows or out.shape[1] != cols:
+        raise ValueError(f"out must be {rows} x {cols}, got {tuple(out.shape)}")
     return out
 
 
@@ -290,13 +311,16 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols:
                      dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values of a rows x cols MXFP4 matrix (fs4_mxfp4_dequantize) in `dtype`, or in `out`."""
     dev = codes.device
-    _mx_check_operand((codes, scales), rows, cols, tiled, "the matrix's", dev)
-    with _on(dev, stream) as handle:
-        y = _mx_out(out, (rows, cols), dtype, dev)
+    _mx_check((codes, scales), rows, cols, tiled, "codes and scales", dev)
+
+    def body(handle):
+        y = _mx_out(out, rows, cols, dtype, dev)
         check(_lib.lib().fs4_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, y.data_ptr(),
                                               _DTYPES[y.dtype], _ld(y), FS4_LAYOUT_TILED if tiled else 0, handle),
               "fs4_mxfp4_dequantize")
-    return y
+        return y
+
+    return _on(dev, stream, body)
 
 
 def mxfp4_gemm(a, b, M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
@@ -305,21 +329,23 @@ def mxfp4_gemm(a, b, M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16
     scales) in the TILED layout, A M x K and B N x K.  A workspace of the caller's is zeroed
     once, before its first call."""
     dev = a[0].device
-    _mx_check_operand(a, M, K, True, "a", dev)
-    _mx_check_operand(b, N, K, True, "b", dev)
+    _mx_check(a, M, K, True, "a", dev)
+    _mx_check(b, N, K, True, "b", dev)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    with _on(dev, stream) as handle:
-        d = _mx_out(out, (M, N), dtype, dev)
-        if workspace is None:
-            workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+    if workspace is not None:
         _check_bytes(workspace, 256, "workspace", dev)
+
+    def body(handle):
+        d = _mx_out(out, M, N, dtype, dev)
+        ws = torch.zeros(256, dtype=torch.uint8, device=dev) if workspace is None else workspace
         check(_lib.lib().fs4_mxfp4_gemm(a[0].data_ptr(), a[1].data_ptr(), b[0].data_ptr(), b[1].data_ptr(), M, N, K,
                                         d.data_ptr(), _DTYPES[d.dtype], _ld(d),
-                                        _lib.FS4_MX_ACCUMULATE if accumulate else 0, workspace.data_ptr(),
-                                        workspace.numel(), handle),
+                                        _lib.FS4_MX_ACCUMULATE if accumulate else 0, ws.data_ptr(), ws.numel(), handle),
               "fs4_mxfp4_gemm")
-    return d
+        return d
+
+    return _on(dev, stream, body)
 
 
 def mxfp4_linear_workspace_size(M: int, K: int) -> int:
@@ -334,22 +360,27 @@ def mxfp4_linear(x: torch.Tensor, w, N: int, dtype: torch.dtype | None = None, s
     _check_matrix(x, "x")
     M, K = x.shape
     dev = x.device
-    _mx_check_operand(w, N, K, True, "w", dev)
+    _mx_check(w, N, K, True, "w", dev)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     flags = _mx_scale_flag(scale_rule) | (_lib.FS4_MX_ACCUMULATE if accumulate else 0)
-    need = mxfp4_linear_workspace_size(M, K)
-    with _on(dev, stream) as handle:
-        d = _mx_out(out, (M, N), x.dtype if dtype is None else dtype, dev)
-        if workspace is None:
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-            workspace[:256].zero_()
+    need = 256 + 17 * mxfp4_tiled_shape(M, K)[1]             # mxfp4_linear_workspace_size(M, K)
+    if workspace is not None:
         _check_bytes(workspace, need, "workspace", dev)
+
+    def body(handle):
+        d = _mx_out(out, M, N, x.dtype if dtype is None else dtype, dev)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+            ws[:256].zero_()
         check(_lib.lib().fs4_mxfp4_linear(x.data_ptr(), _DTYPES[x.dtype], M, K, _ld(x), w[0].data_ptr(),
                                           w[1].data_ptr(), N, d.data_ptr(), _DTYPES[d.dtype], _ld(d), flags,
-                                          workspace.data_ptr(), workspace.numel(), handle),
+                                          ws.data_ptr(), ws.numel(), handle),
               "fs4_mxfp4_linear")
-    return d
+        return d
+
+    return _on(dev, stream, body)
 
 
 def muon_workspace_size(shapes: Sequence[tuple[int, int]]) -> int:
@@ -401,10 +432,13 @@ def muon_orthogonalize(Gs: Sequence[torch.Tensor], K: int = 5, coeffs=MUON_COEFF
         _check_matrix(G, f"Gs[{i}]", dev)
     if outs is not None and len(outs) != len(Gs):
         raise ValueError(f"{len(outs)} outs for {len(Gs)} matrices")
-    with _on(dev, stream) as handle:
-        outs = [_mx_out(None if outs is None else outs[i], G.shape, dtype, dev) for i, G in enumerate(Gs)]
-        _muon_call(outs, Gs, None, [1.0] * len(Gs), K, coeffs, workspace, handle, None)
-    return outs
+
+    def body(handle):
+        res = [_mx_out(None if outs is None else outs[i], *G.shape, dtype, dev) for i, G in enumerate(Gs)]
+        _muon_call(res, Gs, None, [1.0] * len(Gs), K, coeffs, workspace, handle, None)
+        return res
+
+    return _on(dev, stream, body)
 
 
 def _muon_scale(scale, rows: int, cols: int) -> float:
@@ -432,9 +466,9 @@ def muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], mom
             _check_matrix(t, f"{name}[{i}]", dev)
             if t.shape != ts[0].shape:
                 raise ValueError(f"{name}[{i}] must have the shape of params[{i}], {tuple(ts[0].shape)}")
-    with _on(dev, stream) as handle:
-        _muon_call(params, grads, momenta, [_muon_scale(scale, *p.shape) for p in params], K, coeffs, workspace, handle,
-                   (lr, beta, weight_decay, _lib.FS4_MUON_NESTEROV if nesterov else 0))
+    scales = [_muon_scale(scale, *p.shape) for p in params]
+    extra = (lr, beta, weight_decay, _lib.FS4_MUON_NESTEROV if nesterov else 0)
+    _on(dev, stream, lambda handle: _muon_call(params, grads, momenta, scales, K, coeffs, workspace, handle, extra))
 
 
 def _ld(t: torch.Tensor) -> int:

@@ -105,7 +105,7 @@ fs4_status fs4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const
   const fs4_status ds = current_device(&sms);
   if (ds != FS4_OK) return ds;
   MxGemmArgs g{a_codes, a_scales, b_codes, b_scales, M, N, K, d, ldd, d_dtype, (flags & FS4_MX_ACCUMULATE) ? 1 : 0,
-               static_cast<uint32_t*>(workspace)};
+               static_cast<uint32_t*>(workspace), 0};
   return cuda_status(launch_mxfp4_gemm(g, static_cast<cudaStream_t>(stream), sms));
 }
 
@@ -134,11 +134,19 @@ fs4_status fs4_mxfp4_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K
   // the product's checks come before the quantisation is enqueued
   fs4_status s = check_gemm(codes, scales, w_codes, w_scales, M, N, K, d, d_dtype, ldd, workspace, need);
   if (s != FS4_OK) return s;
+  if (!aligned(x, type_bytes(x_dtype))) return FS4_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((s = current_device(&sms)) != FS4_OK) return s;
+  MxLinearArgs l{x, w_codes, w_scales, M, N, K, ldx, d, ldd, x_dtype, d_dtype, (flags & FS4_MX_ACCUMULATE) ? 1 : 0,
+                 (flags & FS4_MX_SCALE_CEIL) ? 1 : 0, static_cast<uint32_t*>(workspace)};
+  cudaError_t e = cudaSuccess;
+  if (mxfp4_linear_fused(l, static_cast<cudaStream_t>(stream), sms, &e)) return cuda_status(e);
   s = fs4_mxfp4_quantize(x, x_dtype, M, K, ldx, codes, scales, nullptr, nullptr, FS4_LAYOUT_TILED | (flags & FS4_MX_SCALE_CEIL), 0,
                          stream);
   if (s != FS4_OK) return s;
-  return fs4_mxfp4_gemm(codes, scales, w_codes, w_scales, M, N, K, d, d_dtype, ldd, flags & FS4_MX_ACCUMULATE, workspace, need,
-                        stream);
+  MxGemmArgs g{codes, scales, w_codes, w_scales, M, N, K, d, ldd, d_dtype, (flags & FS4_MX_ACCUMULATE) ? 1 : 0,
+               static_cast<uint32_t*>(workspace), 1};
+  return cuda_status(launch_mxfp4_gemm(g, static_cast<cudaStream_t>(stream), sms));
 }
 
 }  // extern "C"

@@ -35,8 +35,22 @@ struct MxGemmArgs {
   int32_t dtype;
   int32_t accumulate;
   uint32_t* status;
+  int32_t after_quantize;   // the launch before quantises A: overlap its end
 };
 cudaError_t launch_mxfp4_pair(const MxGemmArgs& a, cudaStream_t st);   // mxfp4_pair.cu
+// A few rows of x times W in one launch that quantises x on its way; false where x does not fit.
+struct MxLinearArgs {
+  const void* x;
+  const uint8_t* w_codes;
+  const uint8_t* w_scales;
+  int64_t M, N, K, ldx;
+  void* d;
+  int64_t ldd;
+  int32_t x_dtype, d_dtype;
+  int32_t accumulate, ceil_rule;
+  uint32_t* status;
+};
+bool mxfp4_linear_fused(const MxLinearArgs& a, cudaStream_t st, int num_sms, cudaError_t* error);
 cudaError_t launch_mxfp4_gemm(const MxGemmArgs& a, cudaStream_t st, int num_sms);
 
 }  // namespace fs4

@@ -144,6 +144,7 @@ template <typename T, bool kRow, bool kCol, bool kSr>
 __global__ void __launch_bounds__(kMxThreads) mxfp4_quantize_kernel(const __grid_constant__ MxQuantArgs a,
                                                                     int32_t tiles_x) {
   extern __shared__ __align__(16) uint8_t mx_smem[];
+  allow_dependents();
   __shared__ __align__(16) uint8_t row_atom[kAtomBytes];
   __shared__ __align__(16) uint8_t col_atom[kAtomBytes];
   T* tile = reinterpret_cast<T*>(mx_smem);

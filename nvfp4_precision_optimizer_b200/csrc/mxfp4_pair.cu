@@ -49,6 +49,7 @@ struct PairArgs {
   void* d;
   int64_t ldd;
   int32_t accumulate;
+  int32_t after_quantize;
   uint32_t* status;
 };
 
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_pair_kernel(const __grid_co
   if (warp == 0 && lane == 0) {
     uint32_t s = 0, ph = 0, issued = 0;
     bool ok = true;
+    wait_for_quantize(a.after_quantize);
     for (int32_t u = first; u < total && ok; u += step) {
       int32_t I, J;
       tile_of(a, u, I, J);
@@ -251,12 +253,14 @@ cudaError_t launch_pair(const PairArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = a.after_quantize ? 2 : 1;
   cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
@@ -282,6 +286,7 @@ cudaError_t launch_mxfp4_pair(const MxGemmArgs& g, cudaStream_t st) {
   a.d = g.d;
   a.ldd = g.ldd;
   a.accumulate = g.accumulate;
+  a.after_quantize = g.after_quantize;
   a.status = g.status;
   switch (g.dtype) {
     case kTypeF32: return launch_pair<float>(a, st);
