@@ -31,36 +31,74 @@ int64_t parts_of(int64_t m, int64_t n) {
   return (m + rows - 1) / rows;
 }
 
-// Bases and partial sums of every matrix; returns the workspace's bytes.
-int64_t plan(int32_t count, const int64_t* rows, const int64_t* cols, MuonTable* t) {
-  int64_t parts = 0;
+struct Plan {
+  int64_t bytes = 0;           // of the workspace
+  bool small = false;          // see MuonCall
+  int32_t split_steps = 1;
+  int64_t parts_at = 0, counts_at = 0, counts = 0;
+};
+
+// The plan depends on the sizes only.  Small calls are those whose products fit kMuonSmallUnits
+// tiles of the small kind.
+Plan plan(int32_t count, const int64_t* rows, const int64_t* cols, MuonTable* t) {
+  Plan pl;
+  int64_t parts = 0, updates = 0, grams = 0;
+  auto sides = [&](int32_t i, int32_t& m, int32_t& n) {
+    m = (int32_t)(rows[i] < cols[i] ? rows[i] : cols[i]);
+    n = (int32_t)(rows[i] < cols[i] ? cols[i] : rows[i]);
+  };
+  int32_t m, n;
   for (int32_t i = 0; i < count; ++i) {
     if (t) {
       t->mat[i].partial = parts;
       t->mat[i].parts = (int32_t)parts_of(rows[i], cols[i]);
     }
     parts += parts_of(rows[i], cols[i]);
+    sides(i, m, n);
+    if (m <= kMuonThin) continue;
+    updates += (int64_t)muon_row_tiles(m) * muon_steps(n);
+    grams += muon_gram_tiles(m);
   }
+  pl.small = updates > 0 && updates <= kMuonSmallUnits && grams <= kMuonSmallUnits;
   int64_t off = up(kMuonPartials + 8 * parts, 1024);
+  if (pl.small) {
+    // the shortest parts, of 8 steps at least, that keep the Gram products' units in bounds
+    for (pl.split_steps = 8;; pl.split_steps += 4) {
+      grams = 0;
+      for (int32_t i = 0; i < count; ++i) {
+        sides(i, m, n);
+        if (m > kMuonThin) grams += muon_gram_tiles(m) * muon_splits(muon_steps(n), pl.split_steps);
+      }
+      if (grams <= kMuonSmallUnits) break;
+    }
+    pl.counts = grams;
+    pl.counts_at = off;
+    pl.parts_at = up(off + 4 * grams, 1024);
+    off = pl.parts_at + grams * (128 * 64 * 4);
+  }
   for (int32_t i = 0; i < count; ++i) {
-    const int64_t m = rows[i] < cols[i] ? rows[i] : cols[i], n = rows[i] < cols[i] ? cols[i] : rows[i];
+    sides(i, m, n);
     if (t) t->mat[i].base = off;
     off = up(off + (m <= kMuonThin ? thin_bytes(m, n) : muon_layout(up(m, kMuonPad), up(n, kMuonPad)).end), 1024);
   }
-  return off;
+  pl.bytes = off;
+  return pl;
 }
 
 // Work units of a matrix in each kernel.  Thin matrices need no norm (their Gram matrix has
 // it), so no pass of their own without a momentum.
-int64_t units_of(const MuonMat& m, int kind) {
+int64_t units_of(const MuonMat& m, int kind, const Plan& pl) {
   const bool thin = m.m <= kMuonThin;
   const int64_t T = m.mp / 256;
   switch (kind) {
     case kUnitsMoment: return !thin || m.mom ? m.parts : 0;
     case kUnitsThin: return thin ? thin_chunks(m.n) : 0;
     case kUnitsPrepare: return thin ? 0 : (int64_t)(m.mp / 128) * (m.np / 64);
-    case kUnitsGram: return thin ? 0 : T * (T + 1) / 2;
-    default: return thin ? 0 : T * (m.np / 256);
+    case kUnitsGram:
+      if (pl.small && !thin) return muon_gram_tiles(m.m) * muon_splits(muon_steps(m.n), pl.split_steps);
+      [[fallthrough]];
+    case kUnitsSquare: return thin ? 0 : pl.small ? muon_gram_tiles(m.m) : T * (T + 1) / 2;
+    default: return thin ? 0 : pl.small ? (int64_t)muon_row_tiles(m.m) * muon_steps(m.n) : T * (m.np / 256);
   }
 }
 
@@ -108,7 +146,8 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
     out[outs++] = range_of(d.w, d.rows, d.cols, d.ld_w, d.w_dtype);
     if (step) out[outs++] = range_of(d.m, d.rows, d.cols, d.ld_m, d.m_dtype);
   }
-  const int64_t need = plan(count, rows, cols, &t);
+  const Plan pl = plan(count, rows, cols, &t);
+  const int64_t need = pl.bytes;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < (size_t)need) return FS4_ERR_WORKSPACE;
   const Range ws{reinterpret_cast<uintptr_t>(workspace), reinterpret_cast<uintptr_t>(workspace) + (uintptr_t)need};
   for (int32_t i = 0; i < outs; ++i) {
@@ -129,7 +168,7 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
     int64_t acc = 0;
     t.prefix[kind][0] = 0;
     for (int32_t i = 0; i < count; ++i) {
-      acc += units_of(t.mat[i], kind);
+      acc += units_of(t.mat[i], kind, pl);
       if (acc > 0x7FFFFFFF) return FS4_ERR_SHAPE;
       t.prefix[kind][i + 1] = (int32_t)acc;
     }
@@ -144,12 +183,20 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
   c.rest = (float)(1.0 - beta);
   c.rate = step ? (float)lr : -1.0f;
   c.keep = step ? (float)(1.0 - lr * weight_decay) : 0.0f;
+  c.small = pl.small ? 1 : 0;
+  c.split_steps = pl.split_steps;
+  c.parts_at = pl.parts_at;
+  c.counts_at = pl.counts_at;
+  c.counts = (int32_t)pl.counts;
   std::memcpy(c.coeffs, coeffs, sizeof(float) * 3 * n_coeffs);
   if (launch_muon_moment(c, t, st) != cudaSuccess) return FS4_ERR_CUDA;
   if (t.prefix[kUnitsThin][count] && launch_muon_thin(c, t.prefix[kUnitsThin][count], st) != cudaSuccess) return FS4_ERR_CUDA;
   if (t.prefix[kUnitsPrepare][count]) {
     if (launch_muon_prepare(c, t.prefix[kUnitsPrepare][count], st, sms) != cudaSuccess) return FS4_ERR_CUDA;
-    if (launch_muon_iterate(c, need, t.prefix[kUnitsGram][count], t.prefix[kUnitsUpdate][count], st) != cudaSuccess) return FS4_ERR_CUDA;
+    int32_t units = 0;
+    for (int kind : {kUnitsGram, kUnitsSquare, kUnitsUpdate})
+      if (t.prefix[kind][count] > units) units = t.prefix[kind][count];
+    if (launch_muon_iterate(c, need, units, st, sms) != cudaSuccess) return FS4_ERR_CUDA;
   }
   return FS4_OK;
 }
@@ -162,7 +209,7 @@ size_t fs4_muon_workspace_size(int32_t count, const int64_t* rows, const int64_t
   if (count < 1 || count > kMuonMaxBatch || !rows || !cols) return 0;
   for (int32_t i = 0; i < count; ++i)
     if (!shape_ok(rows[i], cols[i])) return 0;
-  return (size_t)plan(count, rows, cols, nullptr);
+  return (size_t)plan(count, rows, cols, nullptr).bytes;
 }
 
 fs4_status fs4_muon_orthogonalize(int32_t count, const fs4_muon_desc* descs, int32_t K, const float* coeffs, int32_t n_coeffs,

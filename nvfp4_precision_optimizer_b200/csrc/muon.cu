@@ -32,7 +32,7 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
 }
 
 // Unit u of a matrix: whole rows of G.  CTA 0 also leaves the table
-// in the workspace and resets the status word and the iterate kernel's barrier.
+// in the workspace and resets the status word and the iterate kernel's counts.
 template <int N>
 __global__ void __launch_bounds__(kThreads) muon_moment_kernel(const __grid_constant__ MuonCall p,
                                                                const __grid_constant__ MuonTableN<N> t) {
@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kThreads) muon_moment_kernel(const __grid_cons
     for (int i = threadIdx.x; i < kUnitKinds * (p.count + 1); i += kThreads)
       out->prefix[i / (p.count + 1)][i % (p.count + 1)] = t.prefix[i / (p.count + 1)][i % (p.count + 1)];
     for (int i = threadIdx.x; i < p.count; i += kThreads) out->mat[i] = t.mat[i];
+    for (int i = threadIdx.x; i < p.counts; i += kThreads) reinterpret_cast<uint32_t*>(p.ws + p.counts_at)[i] = 0u;
     if (threadIdx.x == 0) {
       *muon_status(p.ws) = 0u;
       *muon_barrier(p.ws) = 0u;

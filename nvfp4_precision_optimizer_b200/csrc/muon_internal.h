@@ -39,7 +39,7 @@ struct MuonMat {
 };
 
 // Work units of each kernel and matrix, as prefix sums.
-enum MuonUnits { kUnitsMoment = 0, kUnitsThin, kUnitsPrepare, kUnitsGram, kUnitsUpdate, kUnitKinds };
+enum MuonUnits { kUnitsMoment = 0, kUnitsThin, kUnitsPrepare, kUnitsGram, kUnitsSquare, kUnitsUpdate, kUnitKinds };
 
 template <int N>
 struct MuonTableN {
@@ -58,6 +58,10 @@ struct MuonCall {
   int32_t nesterov;
   float beta, rest;        // momentum and 1 - momentum
   float keep, rate;        // weights <- keep * weights - rate * scale * X_K; rate < 0: output = scale * X_K
+  int32_t small;           // the iterate kernel on single CTAs (128 x 64 tiles) instead of pairs
+  int32_t split_steps;     // small: 64-element K steps of one part of a split Gram product
+  int64_t parts_at, counts_at;   // small: partial tiles and their counts, bytes into the workspace
+  int32_t counts;
   float coeffs[3 * FS4_MAX_ITERS];
 };
 
@@ -69,6 +73,22 @@ __host__ __device__ inline uint32_t* muon_status(uint8_t* ws) { return reinterpr
 __host__ __device__ inline uint32_t* muon_barrier(uint8_t* ws) { return reinterpret_cast<uint32_t*>(ws + kMuonBarrier); }
 __host__ __device__ inline MuonTable* muon_table(uint8_t* ws) { return reinterpret_cast<MuonTable*>(ws + kMuonHeader); }
 __host__ __device__ inline double* muon_partials(uint8_t* ws) { return reinterpret_cast<double*>(ws + kMuonPartials); }
+
+// Small calls of the iterate kernel: tiles of 128 rows x 64 columns, only those that hold rows and
+// columns of the matrix (its rows and the columns of A and B in whole 128s: they are K elements).
+constexpr int kMuonSmallUnits = 296;    // most units of a product, two for each of 148 SMs
+__host__ __device__ inline int32_t muon_steps(int32_t k) { return (k + 63) / 64; }
+__host__ __device__ inline int32_t muon_row_tiles(int32_t m) { return (m + 127) / 128; }
+// Tiles of A or B from the diagonal's 256-blocks on.
+__host__ __device__ inline int64_t muon_gram_tiles(int32_t m) {
+  const int64_t r = muon_row_tiles(m), h = r / 2;
+  return 2 * r * r - 4 * (h * (h - 1) + (r & 1 ? h : 0));
+}
+// Parts of a Gram product with `steps` K steps at `per` a part: adding the parts up costs about
+// as much as twelve steps.
+__host__ __device__ inline int32_t muon_splits(int32_t steps, int32_t per) {
+  return steps < per + 12 ? 1 : (steps + per - 1) / per;
+}
 
 // Byte offsets inside a matrix's block: X high parts (two, by iteration parity) and low part,
 // A high and low, B, then the diagonals of A and B (FP32).  Matrices in the TILED BF16 layout
@@ -102,6 +122,6 @@ __host__ __device__ inline int64_t thin_bytes(int64_t m, int64_t n) { return thi
 cudaError_t launch_muon_moment(const MuonCall& c, const MuonTable& t, cudaStream_t st);
 cudaError_t launch_muon_thin(const MuonCall& c, int32_t units, cudaStream_t st);
 cudaError_t launch_muon_prepare(const MuonCall& c, int32_t units, cudaStream_t st, int num_sms);
-cudaError_t launch_muon_iterate(const MuonCall& c, int64_t ws_bytes, int32_t gram_units, int32_t update_units, cudaStream_t st);
+cudaError_t launch_muon_iterate(const MuonCall& c, int64_t ws_bytes, int32_t units, cudaStream_t st, int num_sms);
 
 }  // namespace fs4

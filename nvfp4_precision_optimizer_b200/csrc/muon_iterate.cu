@@ -16,10 +16,13 @@
 // stored.  A block below it is read as its mirror image with the operand's M or N index
 // fastest, which the tensor core takes directly; so is X as the second operand of the update,
 // whose rows are its K index.  Nothing is stored twice.
-// Structure.  A pair of CTAs computes a 256 x 256 block, 128 rows and 256 TMEM columns each;
+// Structure.  Large calls: a pair of CTAs computes a 256 x 256 block, 128 rows and 256 TMEM columns each;
 // either operand's 256 rows are split over the two, so that a 64-deep stage costs each SM 32 KB
 // for 512 cycles of MMAs (a single CTA's 128 x 256 tile would cost 48 KB, more than the 67
-// bytes a cycle that L2 delivers to an SM).  Two accumulators: a block's epilogue overlaps the
+// bytes a cycle that L2 delivers to an SM).  Small calls, whose few blocks would leave most SMs
+// idle and whose time is the sum of latencies: single CTAs on 128 x 64 tiles, a quarter of the
+// epilogue each, only over the rows and columns that the matrices have; a long Gram product is
+// split along K, the partial tiles summed in order by the CTA that finishes last.  Two accumulators: a block's epilogue overlaps the
 // next block's MMAs.  Both CTAs' copies count on the leader's barrier (tensor maps allow that);
 // a relay through the other CTA's threads took 1300 cycles a stage.  Between products the
 // launch's CTAs meet at a counter in the workspace (a cooperative launch: all are resident; the
@@ -36,96 +39,159 @@ namespace fs4 {
 namespace {
 
 constexpr int kThreads = 320;               // warp 0 producer, warp 1 MMA issuer, warps 2-9 epilogue
-constexpr int kStages = 6;
-constexpr int kOperand = 16384;             // bytes of one operand's half in a stage: 128 rows x 64 k
-constexpr int kStage = 2 * kOperand;
-constexpr uint32_t kCols = 512;             // two 256-column accumulators
+constexpr int kTileBytes16 = 16384;         // 128 rows x 64 FP16 elements
 constexpr int kGroup = 8;                   // block rows of a raster group: pairs at work share operands in L2
+
+// kPair: 256 x 256 blocks on CTA pairs; else 128 x 64 tiles on single CTAs.
+template <bool kPair>
+struct Tile {
+  static constexpr int kN = kPair ? 256 : 64;              // columns of an accumulator
+  static constexpr int kA = 16384, kB = kPair ? 16384 : 8192;   // a stage's operands in one CTA, 64 k
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = kPair ? 6 : 8;
+  static constexpr uint32_t kCols = 2 * kN;                // two accumulators
+  static constexpr int kWarpCols = kN / 2;                 // columns of one epilogue warp
+};
 
 // What the roles need of a matrix, in shared memory.
 struct Block {
   int64_t base;
-  int32_t mp, np;
+  int32_t m, n;
 };
 struct Shared {
-  uint64_t full[kStages];      // leader: both CTAs' operands of a stage landed
-  uint64_t empty[kStages];     // the MMAs reading the stage finished (both CTAs)
+  uint64_t full[8];            // (pairs: in the leader) the operands of a stage landed
+  uint64_t empty[8];           // the MMAs reading the stage finished (both CTAs)
   uint64_t acc_full[2];
-  uint64_t acc_empty[2];       // leader: both CTAs drained the accumulator
+  uint64_t acc_empty[2];       // (leader) the accumulator is drained
   uint64_t go;                 // the producer saw every CTA finish the product before
   uint64_t done;
   uint32_t tmem;
   int32_t abort;
+  int32_t arrived;             // CTAs that had finished their part of a split product
   alignas(16) float diag[8][128];   // an epilogue warp's columns of A's diagonal
-  int32_t prefix[2][kMuonMaxBatch + 1];   // units of the Gram products and of the update
+  int32_t prefix[3][kMuonMaxBatch + 1];   // units of the three products
   Block block[kMuonMaxBatch];
 };
-constexpr int kSmem = 1024 + kStages * kStage + (int)sizeof(Shared);
-static_assert(kSmem <= 232448, "over the per-CTA shared-memory limit");
-static_assert(offsetof(Shared, diag) % 16 == 0 && kStages * kStage % 1024 == 0, "read and written 16 bytes at a time");
+template <bool kPair>
+constexpr int kSmem = 1024 + Tile<kPair>::kStages * Tile<kPair>::kStage + (int)sizeof(Shared);
+static_assert(kSmem<true> <= 232448 && kSmem<false> <= 232448, "over the per-CTA shared-memory limit");
+static_assert(offsetof(Shared, diag) % 16 == 0 && Tile<true>::kStage % 1024 == 0 && Tile<false>::kStage % 1024 == 0,
+              "read and written 16 bytes at a time");
 
 enum { kGram = 0, kSquare = 1, kUpdate = 2 };
 
-// One 256 x 256 output block.
+__device__ __forceinline__ int32_t padded(int32_t v) { return (v + kMuonPad - 1) / kMuonPad * kMuonPad; }
+
+// One unit of work: this CTA's rows and columns of an output block, and its range of K.
 struct Job {
   int mat;
-  int32_t I, J;        // block row and column
-  int32_t steps;       // K / 64
+  int32_t row0, col0;      // first row of this CTA, first column of the accumulator
+  int32_t n0;              // first row of the second operand's part in this CTA
+  int32_t k0, steps;       // K / 64
+  int32_t part, parts;     // of a product split along K
 };
 
-// Unit u of a product.  Within a matrix the blocks go through groups of kGroup block rows,
+// Unit u of a product.  Pairs: within a matrix the blocks go through groups of kGroup block rows,
 // column by column, so that the pairs at work read few operand rows and columns.
-template <int E>
-__device__ __forceinline__ Job make_job(const Shared& sh, int count, int32_t u) {
-  const int32_t* prefix = sh.prefix[E == kUpdate ? 1 : 0];
+template <bool kPair, int E>
+__device__ __forceinline__ Job make_job(const MuonCall& p, const Shared& sh, int32_t u, uint32_t rank) {
+  const int32_t* prefix = sh.prefix[E];
   Job j;
-  j.mat = owner_of(prefix, count, u);
+  j.mat = owner_of(prefix, p.count, u);
   const Block& d = sh.block[j.mat];
   int32_t t = u - prefix[j.mat];
-  const int32_t T = d.mp / 256;
-  if constexpr (E == kUpdate) {
-    const int32_t nj = d.np / 256, g = t / (kGroup * nj), h = min(kGroup, T - kGroup * g);
-    t -= g * kGroup * nj;
-    j.J = t / h;
-    j.I = kGroup * g + t % h;
-    j.steps = d.mp / 64;
-  } else {
-    int32_t r0 = 0;
-    for (;; r0 += kGroup) {                 // blocks on and above the diagonal
-      const int32_t h = min(kGroup, T - r0), tri = h * (h + 1) / 2, size = tri + h * (T - r0 - h);
-      if (t >= size) { t -= size; continue; }
-      if (t >= tri) {
-        j.J = r0 + h + (t - tri) / h;
-        j.I = r0 + (t - tri) % h;
-      } else {
-        int32_t c = 0;
-        while (t > c) t -= ++c;
-        j.J = r0 + c;
-        j.I = r0 + t;
+  j.k0 = 0;
+  j.part = 0;
+  j.parts = 1;
+  j.steps = muon_steps(E == kGram ? d.n : d.m);
+  if constexpr (kPair) {
+    const int32_t T = padded(d.m) / 256;
+    int32_t I, J;
+    if constexpr (E == kUpdate) {
+      const int32_t nj = padded(d.n) / 256, g = t / (kGroup * nj), h = min(kGroup, T - kGroup * g);
+      t -= g * kGroup * nj;
+      J = t / h;
+      I = kGroup * g + t % h;
+    } else {
+      int32_t r0 = 0;
+      for (;; r0 += kGroup) {                 // blocks on and above the diagonal
+        const int32_t h = min(kGroup, T - r0), tri = h * (h + 1) / 2, size = tri + h * (T - r0 - h);
+        if (t >= size) { t -= size; continue; }
+        if (t >= tri) {
+          J = r0 + h + (t - tri) / h;
+          I = r0 + (t - tri) % h;
+        } else {
+          int32_t c = 0;
+          while (t > c) t -= ++c;
+          J = r0 + c;
+          I = r0 + t;
+        }
+        break;
       }
-      break;
     }
-    j.steps = (E == kGram ? d.np : d.mp) / 64;
+    j.row0 = 256 * I + 128 * (int32_t)rank;
+    j.col0 = 256 * J;
+    j.n0 = 256 * J + 128 * (int32_t)rank;
+  } else {
+    if (E == kGram) {
+      j.parts = muon_splits(j.steps, p.split_steps);
+      j.part = t % j.parts;
+      t /= j.parts;
+      if (j.parts > 1) {
+        j.k0 = j.part * p.split_steps;
+        j.steps = min(p.split_steps, j.steps - j.k0);
+      }
+    }
+    const int32_t rows = muon_row_tiles(d.m);
+    int32_t i = 0, c = 0;
+    if constexpr (E == kUpdate) {
+      i = t % rows;
+      c = t / rows;
+    } else {                                  // 64-column tiles from the 256-block on the diagonal on
+      for (;; ++i) {
+        const int32_t size = 2 * rows - 4 * (i >> 1);
+        if (t < size) break;
+        t -= size;
+      }
+      c = 4 * (i >> 1) + t;
+    }
+    j.row0 = 128 * i;
+    j.col0 = j.n0 = 64 * c;
   }
   return j;
 }
 
-// Whether block row `blk` of a symmetric operand at k step `k` is read as its mirror image.
-__device__ __forceinline__ bool mirrored(int32_t blk, int32_t k) { return (k >> 2) < blk; }
+// Whether the 256-block of row (or column) `at` of a symmetric operand at k step `k` is read as
+// its mirror image.
+__device__ __forceinline__ bool mirrored(int32_t at, int32_t k) { return (k >> 2) < (at >> 8); }
 
 struct Maps {
   CUtensorMap rows128, rows64;     // the workspace as 128-byte rows, copied 128 or 64 at a time
 };
 
-// 128 rows of M or N from row0 on, 64 k: one tile.
-__device__ __forceinline__ void load_rows(const Maps& m, uint32_t dst, int64_t src, int32_t cp, int32_t row0, int32_t k, uint32_t bar) {
-  tma_rows_pair(dst, &m.rows128, (int32_t)((src >> 7) + ((int64_t)(row0 >> 7) * (cp >> 6) + k) * 128), bar);
+// Where a CTA's copies go and are counted.
+struct Target {
+  const Maps* maps;
+  const uint8_t* ws;
+  uint64_t* bar;         // single CTAs
+  uint32_t cluster_bar;  // pairs: the leader's
+};
+template <bool kPair, int kRows>
+__device__ __forceinline__ void copy_rows(const Target& t, uint32_t dst, int64_t src) {
+  if constexpr (kPair) tma_rows_pair(dst, kRows == 128 ? &t.maps->rows128 : &t.maps->rows64, (int32_t)(src >> 7), t.cluster_bar);
+  else bulk_g2s_addr(dst, t.ws + src, 128 * kRows, t.bar);
 }
-// 64 stored rows from 64 k on, 128 columns from col0 on: halves of two neighbouring tiles.
-__device__ __forceinline__ void load_columns(const Maps& m, uint32_t dst, int64_t src, int32_t cp, int32_t col0, int32_t k, uint32_t bar) {
-  const int32_t row = (int32_t)((src >> 7) + ((int64_t)(k >> 1) * (cp >> 6) + (col0 >> 6)) * 128 + (k & 1) * 64);
-  tma_rows_pair(dst, &m.rows64, row, bar);
-  tma_rows_pair(dst + kOperand / 2, &m.rows64, row + 128, bar);
+// kRows (64 or 128) rows of M or N from row0 on, 64 k: a tile or half of one.
+template <bool kPair, int kRows>
+__device__ __forceinline__ void load_rows(const Target& t, uint32_t dst, int64_t src, int32_t cp, int32_t row0, int32_t k) {
+  copy_rows<kPair, kRows>(t, dst, src + ((int64_t)(row0 >> 7) * (cp >> 6) + k) * kTileBytes16 + (row0 & 127) * 128);
+}
+// 64 stored rows from 64 k on, kCols (64 or 128) columns from col0 on: halves of neighbouring tiles.
+template <bool kPair, int kCols>
+__device__ __forceinline__ void load_columns(const Target& t, uint32_t dst, int64_t src, int32_t cp, int32_t col0, int32_t k) {
+  const int64_t at = src + ((int64_t)(k >> 1) * (cp >> 6) + (col0 >> 6)) * kTileBytes16 + (k & 1) * (kTileBytes16 / 2);
+#pragma unroll
+  for (int i = 0; i < kCols / 64; ++i) copy_rows<kPair, 64>(t, dst + i * (kTileBytes16 / 2), at + i * kTileBytes16);
 }
 
 // ------------------------------------------------------------------ epilogue
@@ -183,9 +249,9 @@ struct Input {
   Pair h[2], l[2];
 };
 
-// What one epilogue warp (rows 32 quad .. + 31 of this CTA's 128, columns 128 half .. + 127) reads
-// and writes of a block.
-template <int E>
+// What one epilogue warp (rows 32 quad .. + 31 of this CTA's 128, kWarpCols columns) reads and
+// writes of a block.
+template <bool kPair, int E>
 struct Place {
   const uint8_t* in_hi;
   const uint8_t* in_lo;
@@ -197,16 +263,15 @@ struct Place {
   int x6;
   bool swap, diagonal;
 
-  __device__ __forceinline__ Place(const MuonCall& p, const Shared& sh, const Job& j, int it, uint32_t rank, int quad_, int half,
-                                   int lane) {
+  __device__ __forceinline__ Place(const MuonCall& p, const Shared& sh, const Job& j, int it, int quad_, int half, int lane) {
     const Block& d = sh.block[j.mat];
-    const MuonLayout L = muon_layout(d.mp, d.np);
+    const int32_t mp = padded(d.m), np = padded(d.n), cp = E == kUpdate ? np : mp;
+    const MuonLayout L = muon_layout(mp, np);
     uint8_t* ws = p.ws + d.base;
-    const int32_t cp = E == kUpdate ? d.np : d.mp;
     const bool odd = (it & 1) != 0;
-    row = 256 * j.I + 128 * (int32_t)rank + 32 * quad_ + lane;
-    col0 = 256 * j.J + 128 * half;
-    const int64_t tile = ((int64_t)(row >> 7) * (cp >> 6) + (col0 >> 6)) * kOperand + (row & 127) * 128;
+    row = j.row0 + 32 * quad_ + lane;
+    col0 = j.col0 + Tile<kPair>::kWarpCols * half;
+    const int64_t tile = ((int64_t)(row >> 7) * (cp >> 6) + (col0 >> 6)) * kTileBytes16 + (row & 127) * 128;
     in_hi = ws + (E == kUpdate ? (odd ? L.x[1] : L.x[0]) : L.a) + tile;
     in_lo = ws + (E == kUpdate ? L.xl : L.al) + tile;
     out_hi = ws + (E == kUpdate ? (odd ? L.x[0] : L.x[1]) : E == kSquare ? L.b : L.a) + tile;
@@ -215,10 +280,13 @@ struct Place {
     db = reinterpret_cast<float*>(ws + L.db);
     swap = (row & 1) != 0;
     x6 = row & 6;
-    diagonal = E != kUpdate && j.I == j.J;
+    diagonal = E != kUpdate;
   }
-  // 32-byte piece i (0, 1) of the 32 columns from c (0, 32, 64, 96) on
-  __device__ __forceinline__ int piece(int c, int i) const { return (c >> 6) * kOperand + 16 * ((((c & 32) >> 3) + 2 * i) ^ x6); }
+  // 32-byte piece i (0, 1) of the 32 columns from c (a multiple of 32) on
+  __device__ __forceinline__ int piece(int c, int i) const {
+    const int in = (col0 & 32) + c;
+    return (in >> 6) * kTileBytes16 + 16 * ((((in & 32) >> 3) + 2 * i) ^ x6);
+  }
   __device__ __forceinline__ void load(Input& in, int c) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -228,39 +296,44 @@ struct Place {
   }
 };
 
-// Before the accumulator is ready: half of the warp's input and the diagonal entries.
+// Before the accumulator is ready: the first of the warp's input and the diagonal entries.
 struct Ahead {
   Input in[2];
   float own;             // d_i (Square) or a + e_i (Update)
 };
-template <int E>
-__device__ __forceinline__ void look_ahead(const MuonCall& p, const Place<E>& w, Ahead& a, float* diag, int it, int lane) {
+template <bool kPair, int E>
+__device__ __forceinline__ void look_ahead(const MuonCall& p, const Place<kPair, E>& w, Ahead& a, float* diag, int it, int lane) {
   if constexpr (E == kGram) return;
   w.load(a.in[0], 0);
-  w.load(a.in[1], 32);
+  if constexpr (kPair) w.load(a.in[1], 32);
   if constexpr (E == kSquare) {
     a.own = __ldcg(w.da + w.row);
-    const float4 c = __ldcg(reinterpret_cast<const float4*>(w.da + w.col0) + lane);
     __syncwarp();
-    reinterpret_cast<float4*>(diag)[lane] = c;
+    if constexpr (kPair) reinterpret_cast<float4*>(diag)[lane] = __ldcg(reinterpret_cast<const float4*>(w.da + w.col0) + lane);
+    else diag[lane] = __ldcg(w.da + w.col0 + lane);
     __syncwarp();
   } else {
     a.own = p.coeffs[p.n_coeffs == 1 ? 0 : 3 * it] + __ldcg(w.db + w.row);
   }
 }
 
-template <int E>
-__device__ __forceinline__ void epilogue(const MuonCall& p, const Place<E>& w, Ahead& a, const float* diag, const MuonMat* m, int it,
-                                         uint32_t taddr, int lane) {
+template <bool kPair, int E>
+__device__ __forceinline__ void epilogue(const MuonCall& p, const Place<kPair, E>& w, Ahead& a, const float* diag, const MuonMat* m, int it,
+                                         uint32_t taddr, int lane, const float* summed) {
   const bool last = E == kUpdate && it == p.K - 1;
   const float* poly = p.coeffs + (p.n_coeffs == 1 ? 0 : 3 * it);
   const float pb = poly[1], pc = poly[2];
   bool bad = false;
   // (rolled: a block's epilogue runs once per product, and its instructions come from L2)
 #pragma unroll 1
-  for (int c = 0; c < 128; c += 32) {
+  for (int c = 0; c < Tile<kPair>::kWarpCols; c += 32) {
     float v[32];
-    tmem_ld32(taddr + c, v);
+    if (!kPair && E == kGram && summed) {      // a product split along K: the partial sums' sum
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = summed[i];
+    } else {
+      tmem_ld32(taddr + c, v);
+    }
     const int32_t col = w.col0 + c;
     // the 32 x 32 part on the diagonal (whole warps: rows and columns are multiples of 32)
     const bool on = w.diagonal && (w.row & ~31) == col;
@@ -277,8 +350,10 @@ __device__ __forceinline__ void epilogue(const MuonCall& p, const Place<E>& w, A
       }
     } else {
       const Input in = a.in[0];
-      a.in[0] = a.in[1];
-      if (c < 64) w.load(a.in[1], c + 64);       // the input two steps on
+      if constexpr (kPair) {
+        a.in[0] = a.in[1];
+        if (c < 64) w.load(a.in[1], c + 64);       // the input two steps on
+      }
       float e = 0.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -353,39 +428,49 @@ __device__ __forceinline__ bool wait_count(const uint32_t* count, uint32_t targe
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // ------------------------------------------------------------------ roles, one product each
+template <bool kPair>
 struct Ring {
   uint32_t s = 0, ph = 0, issued = 0;
   __device__ __forceinline__ void next() {
     ++issued;
-    if (++s == (uint32_t)kStages) { s = 0; ph ^= 1u; }
+    if (++s == (uint32_t)Tile<kPair>::kStages) { s = 0; ph ^= 1u; }
   }
 };
+// Units are dealt to CTA pairs or CTAs in turn.
+template <bool kPair>
+__device__ __forceinline__ int32_t first_unit() { return kPair ? blockIdx.x >> 1 : blockIdx.x; }
+template <bool kPair>
+__device__ __forceinline__ int32_t unit_step() { return kPair ? gridDim.x >> 1 : gridDim.x; }
 
-template <int E>
-__device__ __forceinline__ bool produce(const MuonCall& p, const Maps& maps, Shared& sh, Ring& ring, int it, uint32_t base,
+template <bool kPair, int E>
+__device__ __forceinline__ bool produce(const MuonCall& p, const Maps& maps, Shared& sh, Ring<kPair>& ring, int it, uint32_t base,
                                         uint32_t rank, volatile int* abort) {
-  const int32_t total = sh.prefix[E == kUpdate ? 1 : 0][p.count];
-  for (int32_t u = blockIdx.x >> 1; u < total; u += gridDim.x >> 1) {
-    const Job j = make_job<E>(sh, p.count, u);
+  using T = Tile<kPair>;
+  const int32_t total = sh.prefix[E][p.count];
+  for (int32_t u = first_unit<kPair>(); u < total; u += unit_step<kPair>()) {
+    const Job j = make_job<kPair, E>(p, sh, u, rank);
     const Block& d = sh.block[j.mat];
-    const MuonLayout L = muon_layout(d.mp, d.np);
+    const int32_t mp = padded(d.m), np = padded(d.n);
+    const MuonLayout L = muon_layout(mp, np);
     const int64_t x = d.base + ((it & 1) ? L.x[1] : L.x[0]);
     const int64_t sym = d.base + (E == kSquare ? L.a : L.b);
-    const int32_t rowI = 256 * j.I + 128 * (int32_t)rank, rowJ = 256 * j.J + 128 * (int32_t)rank;
-    for (int32_t k = 0; k < j.steps; ++k) {
+    for (int32_t i = 0; i < j.steps; ++i) {
+      const int32_t k = j.k0 + i;
       if (!mbar_wait(&sh.empty[ring.s], ring.ph ^ 1u, muon_status(p.ws), abort)) return false;
-      const uint32_t a = base + ring.s * kStage, b = a + kOperand;
-      const uint32_t bar = cluster_map(smem_addr(&sh.full[ring.s]), 0);
-      if (rank == 0) mbar_arrive_expect_tx(&sh.full[ring.s], 2 * kStage);
+      const uint32_t a = base + ring.s * T::kStage, b = a + T::kA;
+      Target t{&maps, p.ws, &sh.full[ring.s], 0u};
+      if constexpr (kPair) t.cluster_bar = cluster_map(smem_addr(&sh.full[ring.s]), 0);
+      if (rank == 0) mbar_arrive_expect_tx(&sh.full[ring.s], (kPair ? 2 : 1) * T::kStage);
+      constexpr int kBRows = T::kB / 128;
       if constexpr (E == kGram) {
-        load_rows(maps, a, x, d.np, rowI, k, bar);
-        load_rows(maps, b, x, d.np, rowJ, k, bar);
+        load_rows<kPair, 128>(t, a, x, np, j.row0, k);
+        load_rows<kPair, kBRows>(t, b, x, np, j.n0, k);
       } else {
-        if (mirrored(j.I, k)) load_columns(maps, a, sym, d.mp, rowI, k, bar);
-        else load_rows(maps, a, sym, d.mp, rowI, k, bar);
-        if constexpr (E == kUpdate) load_columns(maps, b, x, d.np, rowJ, k, bar);
-        else if (mirrored(j.J, k)) load_columns(maps, b, sym, d.mp, rowJ, k, bar);
-        else load_rows(maps, b, sym, d.mp, rowJ, k, bar);
+        if (mirrored(j.row0, k)) load_columns<kPair, 128>(t, a, sym, mp, j.row0, k);
+        else load_rows<kPair, 128>(t, a, sym, mp, j.row0, k);
+        if constexpr (E == kUpdate) load_columns<kPair, kBRows>(t, b, x, np, j.n0, k);
+        else if (mirrored(j.n0, k)) load_columns<kPair, kBRows>(t, b, sym, mp, j.n0, k);
+        else load_rows<kPair, kBRows>(t, b, sym, mp, j.n0, k);
       }
       ring.next();
     }
@@ -393,54 +478,116 @@ __device__ __forceinline__ bool produce(const MuonCall& p, const Maps& maps, Sha
   return true;
 }
 
-template <int E>
-__device__ __forceinline__ bool multiply(const MuonCall& p, Shared& sh, Ring& ring, uint32_t& tl, uint32_t base, uint32_t tmem,
+template <bool kPair, int E>
+__device__ __forceinline__ bool multiply(const MuonCall& p, Shared& sh, Ring<kPair>& ring, uint32_t& tl, uint32_t base, uint32_t tmem,
                                          volatile int* abort) {
-  const uint64_t ra0 = sdesc_sw128(base), rb0 = sdesc_sw128(base + kOperand);
-  const uint64_t ca0 = sdesc_sw128_mn(base, kOperand / 2), cb0 = sdesc_sw128_mn(base + kOperand, kOperand / 2);
-  constexpr uint64_t kStep = kStage >> 4;
-  const int32_t total = sh.prefix[E == kUpdate ? 1 : 0][p.count];
-  for (int32_t u = blockIdx.x >> 1; u < total; u += gridDim.x >> 1, ++tl) {
-    const Job j = make_job<E>(sh, p.count, u);
-    const uint32_t acc = tmem + 256u * (tl & 1u);
+  using T = Tile<kPair>;
+  const uint64_t ra0 = sdesc_sw128(base), rb0 = sdesc_sw128(base + T::kA);
+  const uint64_t ca0 = sdesc_sw128_mn(base, kTileBytes16 / 2), cb0 = sdesc_sw128_mn(base + T::kA, kTileBytes16 / 2);
+  constexpr uint64_t kStep = T::kStage >> 4;
+  const int32_t total = sh.prefix[E][p.count];
+  for (int32_t u = first_unit<kPair>(); u < total; u += unit_step<kPair>(), ++tl) {
+    const Job j = make_job<kPair, E>(p, sh, u, 0);
+    const uint32_t acc = tmem + (uint32_t)T::kN * (tl & 1u);
     if (!mbar_wait_cluster(&sh.acc_empty[tl & 1u], ((tl >> 1) & 1u) ^ 1u, muon_status(p.ws), abort)) return false;
     tc_fence_after();
-    for (int32_t k = 0; k < j.steps; ++k) {
+    for (int32_t i = 0; i < j.steps; ++i) {
+      const int32_t k = j.k0 + i;
       if (!mbar_wait_cluster(&sh.full[ring.s], ring.ph, muon_status(p.ws), abort)) return false;
       tc_fence_after();
-      const bool am = E != kGram && mirrored(j.I, k);
-      const bool bm = E == kUpdate || (E == kSquare && mirrored(j.J, k));
+      const bool am = E != kGram && mirrored(j.row0, k);
+      const bool bm = E == kUpdate || (E == kSquare && mirrored(j.n0, k));
       // 16 k: 32 bytes along a row, or 16 rows of 128 bytes
       const uint64_t da = (am ? ca0 : ra0) + ring.s * kStep, db = (bm ? cb0 : rb0) + ring.s * kStep;
       const uint64_t ia = am ? 128 : 2, ib = bm ? 128 : 2;
-      const uint32_t idesc = idesc_f16(256, 256, am, bm);
+      const uint32_t idesc = idesc_f16(kPair ? 256 : 128, T::kN, am, bm);
 #pragma unroll
-      for (int h = 0; h < 4; ++h) tc_mma_f16_pair(acc, da + h * ia, db + h * ib, idesc, (k | h) != 0 ? 1u : 0u);
-      tc_commit_pair(&sh.empty[ring.s]);
+      for (int h = 0; h < 4; ++h) {
+        if constexpr (kPair) tc_mma_f16_pair(acc, da + h * ia, db + h * ib, idesc, (i | h) != 0 ? 1u : 0u);
+        else tc_mma_bf16(acc, da + h * ia, db + h * ib, idesc, (i | h) != 0 ? 1u : 0u);   // kind::f16: the type is in idesc
+      }
+      if constexpr (kPair) tc_commit_pair(&sh.empty[ring.s]);
+      else tc_commit(&sh.empty[ring.s]);
       ring.next();
     }
-    tc_commit_pair(&sh.acc_full[tl & 1u]);
+    if constexpr (kPair) tc_commit_pair(&sh.acc_full[tl & 1u]);
+    else tc_commit(&sh.acc_full[tl & 1u]);
   }
   return true;
 }
 
-template <int E>
+// A split product's unit: leave this part's sums in the workspace; the CTA that finishes a tile's
+// last part adds all parts up, in their order, into `v` and returns true.
+__device__ __forceinline__ bool sum_parts(const MuonCall& p, Shared& sh, const Job& j, int32_t u, uint32_t taddr, int quad_, int half,
+                                          int lane, float* v) {
+  tmem_ld32(taddr, v);
+  // [unit][row][column]: 128 bytes a lane
+  const int64_t at = ((int64_t)(32 * quad_ + lane) * 64 + 32 * half) * 4;
+  uint8_t* parts = p.ws + p.parts_at;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    Pair r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(v[8 * q + i]);
+    store_pair(parts + (int64_t)u * (128 * 64 * 4) + at + 32 * q, r);
+  }
+  const int32_t first = u - j.part;
+  uint32_t* arrived = reinterpret_cast<uint32_t*>(p.ws + p.counts_at) + first;
+  named_bar(2, 256);
+  if (threadIdx.x == 64) {
+    __threadfence();
+    const uint32_t before = atomicAdd(arrived, 1u);
+    __threadfence();
+    sh.arrived = (int32_t)before;
+    if (before == (uint32_t)j.parts - 1) *arrived = 0u;     // for the next iteration
+  }
+  named_bar(2, 256);
+  if (sh.arrived != j.parts - 1) return false;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+  for (int s = 0; s < j.parts; ++s) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const Pair r = load_pair(parts + (int64_t)(first + s) * (128 * 64 * 4) + at + 32 * q);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * q + i] += __uint_as_float(r.w[i]);
+    }
+  }
+  return true;
+}
+
+template <bool kPair, int E>
 __device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, uint32_t& tl, int it, uint32_t tmem, uint32_t rank, int quad_,
                                        int half, int lane, volatile int* abort) {
-  const int32_t total = sh.prefix[E == kUpdate ? 1 : 0][p.count];
-  for (int32_t u = blockIdx.x >> 1; u < total; u += gridDim.x >> 1, ++tl) {
-    const Job j = make_job<E>(sh, p.count, u);
+  using T = Tile<kPair>;
+  const int32_t total = sh.prefix[E][p.count];
+  for (int32_t u = first_unit<kPair>(); u < total; u += unit_step<kPair>(), ++tl) {
+    const Job j = make_job<kPair, E>(p, sh, u, rank);
     const uint32_t b = tl & 1u;
-    const Place<E> w(p, sh, j, it, rank, quad_, half, lane);
+    const Place<kPair, E> w(p, sh, j, it, quad_, half, lane);
     float* diag = sh.diag[4 * half + quad_];
     Ahead a;
-    look_ahead<E>(p, w, a, diag, it, lane);
+    look_ahead<kPair, E>(p, w, a, diag, it, lane);
     const int got = lane == 0 ? (mbar_wait(&sh.acc_full[b], (tl >> 1) & 1u, muon_status(p.ws), abort) ? 1 : 0) : 0;
-    if (__shfl_sync(0xFFFFFFFFu, got, 0) == 0) return false;
+    bool ok = __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
+    if (!kPair && E == kGram) {
+      // the warps meet in split units: all go on, or none
+      if (!ok && lane == 0) *abort = 1;
+      named_bar(2, 256);
+      ok = *abort == 0;
+      named_bar(2, 256);
+    }
+    if (!ok) return false;
     __syncwarp();
     tc_fence_after();
-    epilogue<E>(p, w, a, diag, &muon_table(p.ws)->mat[j.mat], it,
-                tmem + 256u * b + ((uint32_t)(32 * quad_) << 16) + (uint32_t)(128 * half), lane);
+    const uint32_t taddr = tmem + (uint32_t)T::kN * b + ((uint32_t)(32 * quad_) << 16) + (uint32_t)(T::kWarpCols * half);
+    const MuonMat* m = &muon_table(p.ws)->mat[j.mat];
+    if (!kPair && E == kGram && j.parts > 1) {
+      float v[32];
+      if (sum_parts(p, sh, j, u, taddr, quad_, half, lane, v)) epilogue<kPair, E>(p, w, a, diag, m, it, taddr, lane, v);
+    } else {
+      epilogue<kPair, E>(p, w, a, diag, m, it, taddr, lane, nullptr);
+    }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
@@ -451,48 +598,58 @@ __device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, uint32_t& 
   return true;
 }
 
+template <bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_constant__ MuonCall p, const __grid_constant__ Maps maps) {
+  using T = Tile<kPair>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Shared& sh = *reinterpret_cast<Shared*>(smem + kStages * kStage);
+  Shared& sh = *reinterpret_cast<Shared*>(smem + T::kStages * T::kStage);
   volatile int* abort = &sh.abort;
   uint32_t* status = muon_status(p.ws);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = kPair ? cluster_rank() : 0u;
   const MuonTable& t = *muon_table(p.ws);
   for (int i = threadIdx.x; i <= p.count; i += kThreads) {
-    sh.prefix[0][i] = t.prefix[kUnitsGram][i];
-    sh.prefix[1][i] = t.prefix[kUnitsUpdate][i];
-    if (i < p.count) sh.block[i] = Block{t.mat[i].base, t.mat[i].mp, t.mat[i].np};
+    sh.prefix[kGram][i] = t.prefix[kUnitsGram][i];
+    sh.prefix[kSquare][i] = t.prefix[kUnitsSquare][i];
+    sh.prefix[kUpdate][i] = t.prefix[kUnitsUpdate][i];
+    if (i < p.count) sh.block[i] = Block{t.mat[i].base, t.mat[i].m, t.mat[i].n};
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < T::kStages; ++s) {
       mbar_init(&sh.full[s], 1);
       mbar_init(&sh.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.acc_full[b], 1);
-      mbar_init(&sh.acc_empty[b], 16);
+      mbar_init(&sh.acc_empty[b], kPair ? 16 : 8);
     }
     mbar_init(&sh.go, 1);
     mbar_init(&sh.done, 1);
     sh.abort = 0;
     fence_mbar_init();
-    tma_prefetch_map(&maps.rows128);
-    tma_prefetch_map(&maps.rows64);
+    if constexpr (kPair) {
+      tma_prefetch_map(&maps.rows128);
+      tma_prefetch_map(&maps.rows64);
+    }
   }
-  if (warp == 1) tmem_alloc_pair(&sh.tmem, kCols);
+  if (warp == 1) {
+    if constexpr (kPair) tmem_alloc_pair(&sh.tmem, T::kCols);
+    else tmem_alloc(&sh.tmem, T::kCols);
+  }
   tc_fence_before();
   __syncthreads();
-  cluster_arrive();
-  cluster_wait();
+  if constexpr (kPair) {
+    cluster_arrive();
+    cluster_wait();
+  }
   tc_fence_after();
   const uint32_t tmem = sh.tmem, base = smem_addr(smem);
   const uint32_t* count = muon_barrier(p.ws);
 
   if (warp == 0) {
     if (lane == 0) {
-      Ring ring;
+      Ring<kPair> ring;
       bool ok = true;
       for (int ph = 0; ph < 3 * p.K && ok; ++ph) {
         if (ph > 0) {
@@ -502,30 +659,31 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
           fence_async();
         }
         const int it = ph / 3, e = ph - 3 * it;
-        ok = e == kGram ? produce<kGram>(p, maps, sh, ring, it, base, rank, abort)
-             : e == kSquare ? produce<kSquare>(p, maps, sh, ring, it, base, rank, abort)
-                            : produce<kUpdate>(p, maps, sh, ring, it, base, rank, abort);
+        ok = e == kGram ? produce<kPair, kGram>(p, maps, sh, ring, it, base, rank, abort)
+             : e == kSquare ? produce<kPair, kSquare>(p, maps, sh, ring, it, base, rank, abort)
+                            : produce<kPair, kUpdate>(p, maps, sh, ring, it, base, rank, abort);
       }
       // every copy lands before the pair may exit (they count on the leader's barriers)
       if (rank == 0) {
-        for (uint32_t i = ring.issued > (uint32_t)kStages ? ring.issued - kStages : 0u; i < ring.issued; ++i) {
+        for (uint32_t i = ring.issued > (uint32_t)T::kStages ? ring.issued - T::kStages : 0u; i < ring.issued; ++i) {
           volatile int never = 0;
-          mbar_wait(&sh.full[i % kStages], (i / kStages) & 1u, status, &never);
+          mbar_wait(&sh.full[i % T::kStages], (i / T::kStages) & 1u, status, &never);
         }
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      Ring ring;
+      Ring<kPair> ring;
       uint32_t tl = 0;
       bool ok = true;
       for (int ph = 0; ph < 3 * p.K && ok; ++ph) {
         const int e = ph % 3;
-        ok = e == kGram ? multiply<kGram>(p, sh, ring, tl, base, tmem, abort)
-             : e == kSquare ? multiply<kSquare>(p, sh, ring, tl, base, tmem, abort)
-                            : multiply<kUpdate>(p, sh, ring, tl, base, tmem, abort);
+        ok = e == kGram ? multiply<kPair, kGram>(p, sh, ring, tl, base, tmem, abort)
+             : e == kSquare ? multiply<kPair, kSquare>(p, sh, ring, tl, base, tmem, abort)
+                            : multiply<kPair, kUpdate>(p, sh, ring, tl, base, tmem, abort);
       }
-      tc_commit_pair(&sh.done);
+      if constexpr (kPair) tc_commit_pair(&sh.done);
+      else tc_commit(&sh.done);
       volatile int never = 0;
       mbar_wait(&sh.done, 0, status, &never);
     }
@@ -541,9 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
         __syncwarp();
       }
       if (ok)
-        ok = e == kGram ? finish<kGram>(p, sh, tl, it, tmem, rank, quad_, half, lane, abort)
-             : e == kSquare ? finish<kSquare>(p, sh, tl, it, tmem, rank, quad_, half, lane, abort)
-                            : finish<kUpdate>(p, sh, tl, it, tmem, rank, quad_, half, lane, abort);
+        ok = e == kGram ? finish<kPair, kGram>(p, sh, tl, it, tmem, rank, quad_, half, lane, abort)
+             : e == kSquare ? finish<kPair, kSquare>(p, sh, tl, it, tmem, rank, quad_, half, lane, abort)
+                            : finish<kPair, kUpdate>(p, sh, tl, it, tmem, rank, quad_, half, lane, abort);
       // every thread's results before the count (the barrier orders them before the release);
       // a producer that sees the count fences its TMA copies behind it
       named_bar(1, 256);
@@ -554,43 +712,64 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
     }
   }
   __syncwarp();
-  // the leader's MMAs read the other CTA's memory: neither leaves before both are done
+  // (pairs) the leader's MMAs read the other CTA's memory: neither leaves before both are done
   tc_fence_before();
   __syncthreads();
-  cluster_arrive();
-  cluster_wait();
+  if constexpr (kPair) {
+    cluster_arrive();
+    cluster_wait();
+  }
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, kCols);
-  __syncthreads();
-  cluster_arrive();
-  cluster_wait();
+  if (warp == 1) {
+    if constexpr (kPair) tmem_dealloc_pair(tmem, T::kCols);
+    else tmem_dealloc(tmem, T::kCols);
+  }
+  if constexpr (kPair) {
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_muon_iterate(const MuonCall& c, int64_t ws_bytes, int32_t gram_units, int32_t update_units, cudaStream_t st) {
-  static PairSlots slots;
-  int pairs = 0;
-  cudaError_t e = pair_slots(slots, muon_iterate_kernel, kThreads, kSmem, &pairs);
-  if (e != cudaSuccess) return e;
-  Maps maps;
-  if ((e = make_row_map(&maps.rows128, c.ws, ws_bytes / 128 * 128, 128)) != cudaSuccess) return e;
-  if ((e = make_row_map(&maps.rows64, c.ws, ws_bytes / 128 * 128, 64)) != cudaSuccess) return e;
-  const int32_t units = gram_units > update_units ? gram_units : update_units;
+cudaError_t launch_muon_iterate(const MuonCall& c, int64_t ws_bytes, int32_t units, cudaStream_t st, int num_sms) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeCooperative;
-  at[1].val.cooperative = 1;
+  at[0].id = cudaLaunchAttributeCooperative;
+  at[0].val.cooperative = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  Maps maps{};
+  cudaError_t e;
+  if (c.small) {
+    static PairSlots set;       // devices whose shared-memory limit is raised
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (set.pairs[dev] == 0) {
+      if ((e = cudaFuncSetAttribute(muon_iterate_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<false>)) != cudaSuccess)
+        return e;
+      set.pairs[dev] = 1;
+    }
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)(units < num_sms ? units : num_sms));
+    cfg.dynamicSmemBytes = kSmem<false>;
+    return cudaLaunchKernelEx(&cfg, muon_iterate_kernel<false>, c, maps);
+  }
+  static PairSlots slots;
+  int pairs = 0;
+  if ((e = pair_slots(slots, muon_iterate_kernel<true>, kThreads, kSmem<true>, &pairs)) != cudaSuccess) return e;
+  if ((e = make_row_map(&maps.rows128, c.ws, ws_bytes / 128 * 128, 128)) != cudaSuccess) return e;
+  if ((e = make_row_map(&maps.rows64, c.ws, ws_bytes / 128 * 128, 64)) != cudaSuccess) return e;
   cfg.numAttrs = 2;
   cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = st;
-  return cudaLaunchKernelEx(&cfg, muon_iterate_kernel, c, maps);
+  cfg.dynamicSmemBytes = kSmem<true>;
+  return cudaLaunchKernelEx(&cfg, muon_iterate_kernel<true>, c, maps);
 }
 
 }  // namespace fs4

@@ -13,7 +13,8 @@ pytestmark = pytest.mark.gpu
 
 TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 NEAR = 2.0 ** -9
-SHAPES = [(1, 1), (1, 40), (40, 1), (2, 3), (16, 16), (31, 33), (128, 256), (257, 255), (300, 1111), (1030, 129), (513, 520)]
+SHAPES = [(1, 1), (1, 40), (40, 1), (2, 3), (16, 16), (31, 33), (128, 256), (257, 255), (300, 1111), (1030, 129), (513, 520), (33, 8190),
+          (129, 4100), (2050, 70), (1100, 1300)]
 
 
 def half_step(t):

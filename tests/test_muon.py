@@ -87,9 +87,12 @@ def test_workspace_sizes(F):
     assert F.muon_workspace_size([(16, 16)] * 225) == 0
     a, b = F.muon_workspace_size([(300, 1000)]), F.muon_workspace_size([(1000, 300)])
     # X in three FP16 parts, A in two and B in one, and two diagonals, on sizes padded to 256,
-    # beside the table of matrices and the partial sums
+    # beside the table of matrices, the partial sums and, for a small call, at most 296 partial
+    # tiles of 32 KB
     floor = 6 * 512 * 1024 + 6 * 512 * 512 + 8 * 512
-    assert floor < a <= floor + (1 << 16) and floor < b <= floor + (1 << 16)
+    assert floor < a <= floor + (1 << 16) + 296 * 32768 and floor < b <= floor + (1 << 16) + 296 * 32768
+    big, block = F.muon_workspace_size([(4096, 4096)] * 3), 12 * 4096 * 4096 + 8 * 4096
+    assert 3 * block < big <= 3 * block + (1 << 17)
 
 
 def test_binding_refusals(F):
