@@ -31,10 +31,25 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return s;
 }
 
+// Sum of eight squares, in FP64 where FP32 could overflow or lose small ones.
+__device__ __forceinline__ double squares8(const float* u) {
+  float s = 0.0f, m = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    s = fmaf(u[k], u[k], s);
+    m = fmaxf(m, fabsf(u[k]));
+  }
+  if (m < 1e18f && (m > 1e-15f || m == 0.0f) && s == s) return (double)s;
+  double e = 0.0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) e += (double)u[k] * (double)u[k];
+  return e;
+}
+
 // Unit u of a matrix: whole rows of G.  CTA 0 also leaves the table
 // in the workspace and resets the status word and the iterate kernel's counts.
 template <int N>
-__global__ void __launch_bounds__(kThreads) muon_moment_kernel(const __grid_constant__ MuonCall p,
+__global__ void __launch_bounds__(kThreads, 2) muon_moment_kernel(const __grid_constant__ MuonCall p,
                                                                const __grid_constant__ MuonTableN<N> t) {
   __shared__ double red[kThreads / 32];
   if (blockIdx.x == 0) {
@@ -59,30 +74,39 @@ __global__ void __launch_bounds__(kThreads) muon_moment_kernel(const __grid_cons
   const bool vec = gcols % 8 == 0 && aligned16(d.g, d.ldg, d.tg) && (!d.mom || aligned16(d.mom, d.ldm, d.tm));
   double sum = 0.0;
   if (vec) {
+    // rows without gaps need no division into rows and columns
+    const bool flat = d.ldg == gcols && (!d.mom || d.ldm == gcols);
     const int32_t width = gcols / 8, count = (r1 - r0) * width;
+    auto at = [&](int32_t i, int64_t ld) -> int64_t {
+      return flat ? (int64_t)r0 * gcols + 8ll * i : (r0 + i / width) * ld + 8 * (i % width);
+    };
     for (int32_t i0 = threadIdx.x; i0 < count; i0 += kAhead * kThreads) {
-      float g[kAhead][8], m[kAhead][8];
+      Raw8 g[kAhead], m[kAhead];
 #pragma unroll
       for (int s = 0; s < kAhead; ++s) {
         const int32_t i = i0 + s * kThreads;
-        if (i >= count) break;
-        const int64_t r = r0 + i / width, c = 8 * (i % width);
-        get8(d.g, r * d.ldg + c, d.tg, g[s]);
-        if (d.mom) get8(d.mom, r * d.ldm + c, d.tm, m[s]);
+        if (i < count) {
+          g[s] = load8(d.g, at(i, d.ldg), d.tg);
+          if (d.mom) m[s] = load8(d.mom, at(i, d.ldm), d.tm);
+        }
       }
 #pragma unroll
       for (int s = 0; s < kAhead; ++s) {
         const int32_t i = i0 + s * kThreads;
-        if (i >= count) break;
-        if (d.mom) {
+        if (i < count) {
+          float u[8];
+          unpack8(g[s], d.tg, u);
+          if (d.mom) {
+            float v[8];
+            unpack8(m[s], d.tm, v);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) m[s][k] = fmaf(p.beta, m[s][k], p.rest * g[s][k]);
-          put8(d.mom, (int64_t)(r0 + i / width) * d.ldm + 8 * (i % width), d.tm, m[s]);
+            for (int k = 0; k < 8; ++k) v[k] = fmaf(p.beta, v[k], p.rest * u[k]);
+            put8(d.mom, at(i, d.ldm), d.tm, v);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) g[s][k] = direction(p, m[s][k], g[s][k]);
+            for (int k = 0; k < 8; ++k) u[k] = direction(p, v[k], u[k]);
+          }
+          sum += squares8(u);
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum += (double)g[s][k] * (double)g[s][k];
       }
     }
   } else {
@@ -101,14 +125,25 @@ __global__ void __launch_bounds__(kThreads) muon_moment_kernel(const __grid_cons
   if (threadIdx.x == 0) muon_partials(p.ws)[d.partial + part] = s;
 }
 
-// Eight elements of U from (r, c) of G on; absent ones are 0.
-__device__ __forceinline__ void direction8(const MuonCall& p, const MuonMat& d, bool vec, int64_t r, int64_t c, int64_t rows,
-                                           int64_t cols, float* x) {
-  if (vec && r < rows && c + 8 <= cols) {
-    get8(d.g, r * d.ldg + c, d.tg, x);
+// Eight elements of U from (r, c) of G on: in memory's form, then their values; absent ones are 0.
+struct RawU {
+  Raw8 g, m;
+};
+__device__ __forceinline__ bool whole8(bool vec, int64_t r, int64_t c, int64_t rows, int64_t cols) {
+  return vec && r < rows && c + 8 <= cols;
+}
+__device__ __forceinline__ void load_direction8(const MuonMat& d, bool whole, int64_t r, int64_t c, RawU& x) {
+  if (!whole) return;
+  x.g = load8(d.g, r * d.ldg + c, d.tg);
+  if (d.mom) x.m = load8(d.mom, r * d.ldm + c, d.tm);
+}
+__device__ __forceinline__ void direction8(const MuonCall& p, const MuonMat& d, bool whole, int64_t r, int64_t c, int64_t rows,
+                                           int64_t cols, const RawU& raw, float* x) {
+  if (whole) {
+    unpack8(raw.g, d.tg, x);
     if (d.mom) {
       float m[8];
-      get8(d.mom, r * d.ldm + c, d.tm, m);
+      unpack8(raw.m, d.tm, m);
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] = direction(p, m[k], x[k]);
     }
@@ -121,7 +156,7 @@ __device__ __forceinline__ void direction8(const MuonCall& p, const MuonMat& d, 
 // Persistent, a contiguous range of 128 x 64 tiles of X_0 a CTA.  A tall matrix's tile turns in
 // shared memory: element (c, r) of G at word r ^ 4 (c / 8 % 8) of row c, so that the reads of
 // eight c at one r take different banks.
-__global__ void __launch_bounds__(kThreads) muon_prepare_kernel(const __grid_constant__ MuonCall p) {
+__global__ void __launch_bounds__(kThreads, 2) muon_prepare_kernel(const __grid_constant__ MuonCall p) {
   __shared__ double red[kThreads / 32];
   __shared__ __align__(16) float turn[64 * 128];
   const MuonTable& t = *muon_table(p.ws);
@@ -154,14 +189,26 @@ __global__ void __launch_bounds__(kThreads) muon_prepare_kernel(const __grid_con
     uint8_t* hi = p.ws + d.base + L.x[0];
     uint8_t* lo = p.ws + d.base + L.xl;
     const bool vec = aligned16(d.g, d.ldg, d.tg) && (!d.mom || aligned16(d.mom, d.ldm, d.tm));
+    // rows and columns of G that piece s reads: 128 rows x 8 pieces, or, tall (G is n x m: rows
+    // c0 .., columns r0 ..), 64 rows x 16 pieces
+    const int64_t grows = d.tall ? d.n : d.m, gcols = d.tall ? d.m : d.n;
+    auto row_of = [&](int q) -> int64_t { return d.tall ? c0 + (q >> 4) : r0 + (q >> 3); };
+    auto col_of = [&](int q) -> int64_t { return d.tall ? r0 + 8 * (q & 15) : c0 + 8 * (q & 7); };
     float x[kAhead][8];
-    if (d.tall) {
-      // G is n x m: rows c0 .., columns r0 ..
+    {
+      RawU raw[kAhead];
 #pragma unroll
       for (int s = 0; s < kAhead; ++s) {
-        const int q = threadIdx.x + s * kThreads;      // 64 rows x 16 pieces
-        direction8(p, d, vec, c0 + (q >> 4), r0 + 8 * (q & 15), d.n, d.m, x[s]);
+        const int q = threadIdx.x + s * kThreads;
+        load_direction8(d, whole8(vec, row_of(q), col_of(q), grows, gcols), row_of(q), col_of(q), raw[s]);
       }
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        const int q = threadIdx.x + s * kThreads;
+        direction8(p, d, whole8(vec, row_of(q), col_of(q), grows, gcols), row_of(q), col_of(q), grows, gcols, raw[s], x[s]);
+      }
+    }
+    if (d.tall) {
       __syncthreads();
 #pragma unroll
       for (int s = 0; s < kAhead; ++s) {
@@ -175,12 +222,6 @@ __global__ void __launch_bounds__(kThreads) muon_prepare_kernel(const __grid_con
         const int q = threadIdx.x + s * kThreads, r = q >> 3, c = 8 * (q & 7);
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[s][k] = turn[128 * (c + k) + (r ^ (4 * (q & 7)))];
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < kAhead; ++s) {
-        const int q = threadIdx.x + s * kThreads;      // 128 rows x 8 pieces
-        direction8(p, d, vec, r0 + (q >> 3), c0 + 8 * (q & 7), d.m, d.n, x[s]);
       }
     }
 #pragma unroll

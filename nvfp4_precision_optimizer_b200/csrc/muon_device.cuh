@@ -43,22 +43,37 @@ __device__ __forceinline__ bool aligned16(const void* p, int64_t ld, int type) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * (type == kTypeF32 ? 4 : 2))) & 15) == 0;
 }
 
-// Eight consecutive elements from index i (16-byte aligned).
-__device__ __forceinline__ void get8(const void* p, int64_t i, int type, float* v) {
+// Eight consecutive elements from index i (16-byte aligned) as they are in memory, and their
+// values: apart, so that several loads are in flight before the first is unpacked.
+struct Raw8 {
+  uint4 a, b;
+};
+__device__ __forceinline__ Raw8 load8(const void* p, int64_t i, int type) {
+  Raw8 r;
   if (type == kTypeF32) {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = f[0], b = f[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    return;
+    const uint4* f = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+    r.a = f[0];
+    r.b = f[1];
+  } else {
+    r.a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    r.b = make_uint4(0u, 0u, 0u, 0u);
   }
-  const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  return r;
+}
+__device__ __forceinline__ void unpack8(const Raw8& r, int type, float* v) {
+  const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  if (type == kTypeF32) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (type == kTypeBf16) {
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(u[k]);
+  } else if (type == kTypeBf16) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
       v[2 * k] = __uint_as_float(u[k] << 16);
       v[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
-    } else {
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
       v[2 * k] = half_lo(u[k]);
       v[2 * k + 1] = half_hi(u[k]);
     }
