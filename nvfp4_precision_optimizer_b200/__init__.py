@@ -7,6 +7,7 @@ streams) into those calls.  There is no CPU or fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Sequence
 
@@ -188,19 +189,27 @@ def _check_matrix(x: torch.Tensor, name: str, device: torch.device | None = None
 
 
 def _check_bytes(t: torch.Tensor, need: int, name: str, device: torch.device) -> None:
-    if t.dtype != torch.uint8 or t.device != device or t.numel() < need or not t.is_contiguous():
+    if t.dtype is not torch.uint8 or t.numel() < need or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {need} bytes on {device}")
 
 
-def _on(device: torch.device, stream, body):
-    """body(stream handle) with `device` and `stream` (default: the device's current one) current,
-    so that what a call allocates or zeroes belongs to the stream it runs on."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return body(torch._C._cuda_getCurrentRawStream(device.index))
+def _here(device: torch.device, stream) -> bool:
+    """Whether a call can go to the current stream of the current device."""
+    return stream is None and device.index == torch._C._cuda_getDevice()
+
+
+def _handle(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+@contextlib.contextmanager
+def _at(device: torch.device, stream):
+    """Makes `device` and `stream` (None: the device's current one) current, so that what a call
+    allocates or zeroes belongs to the stream it runs on."""
     if stream is not None and stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
-        return body(torch.cuda.current_stream(device).cuda_stream)
+        yield
 
 
 def mxfp4_tiled_shape(rows: int, cols: int) -> tuple[int, int]:
@@ -240,7 +249,7 @@ def _mx_scale_flag(scale_rule: str) -> int:
     return _lib.FS4_MX_SCALE_CEIL
 
 
-def _mx_quantize(x, row, col, tiled, scale_rule, seed, handle):
+def _mx_quantize(x, row, col, tiled, scale_rule, seed):
     flags = _mx_scale_flag(scale_rule) | (FS4_LAYOUT_TILED if tiled else 0)
     if seed is None:
         seed = 0
@@ -251,7 +260,7 @@ def _mx_quantize(x, row, col, tiled, scale_rule, seed, handle):
     rc, rs = (None, None) if row is None else (row[0].data_ptr(), row[1].data_ptr())
     cc, cs = (None, None) if col is None else (col[0].data_ptr(), col[1].data_ptr())
     check(_lib.lib().fs4_mxfp4_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, cols, _ld(x), rc, rs, cc, cs, flags, seed,
-                                        handle),
+                                        _handle(x.device)),
           "fs4_mxfp4_quantize")
 
 
@@ -262,21 +271,20 @@ def mxfp4_quantize(x: torch.Tensor, axis: int = FS4_AXIS_ROW, tiled: bool = Fals
     saturates nothing; a seed rounds stochastically.  Returns (codes, scales); `out` is such
     a pair to write into."""
     _check_matrix(x, "x")
-    if axis != FS4_AXIS_ROW and axis != FS4_AXIS_COL:
-        raise ValueError(f"axis must be FS4_AXIS_ROW or FS4_AXIS_COL, not {axis}")
     dev = x.device
-
-    def body(handle):
-        rows, cols = x.shape
-        if axis == FS4_AXIS_ROW:
-            view = _mx_view(rows, cols, tiled, dev, out)
-            _mx_quantize(x, view, None, tiled, scale_rule, seed, handle)
-        else:
-            view = _mx_view(cols, rows, tiled, dev, out)
-            _mx_quantize(x, None, view, tiled, scale_rule, seed, handle)
-        return view
-
-    return _on(dev, stream, body)
+    if not _here(dev, stream):
+        with _at(dev, stream):
+            return mxfp4_quantize(x, axis, tiled, scale_rule, seed, out)
+    rows, cols = x.shape
+    if axis == FS4_AXIS_ROW:
+        view = _mx_view(rows, cols, tiled, dev, out)
+        _mx_quantize(x, view, None, tiled, scale_rule, seed)
+    elif axis == FS4_AXIS_COL:
+        view = _mx_view(cols, rows, tiled, dev, out)
+        _mx_quantize(x, None, view, tiled, scale_rule, seed)
+    else:
+        raise ValueError(f"axis must be FS4_AXIS_ROW or FS4_AXIS_COL, not {axis}")
+    return view
 
 
 def mxfp4_quantize_both(x: torch.Tensor, tiled: bool = False, scale_rule: str = "floor", seed: int | None = None,
@@ -285,15 +293,14 @@ def mxfp4_quantize_both(x: torch.Tensor, tiled: bool = False, scale_rule: str = 
     training step needs them.  Returns ((codes, scales) of x, (codes, scales) of x^T)."""
     _check_matrix(x, "x")
     dev = x.device
-
-    def body(handle):
-        rows, cols = x.shape
-        row = _mx_view(rows, cols, tiled, dev, None if out is None else out[0])
-        col = _mx_view(cols, rows, tiled, dev, None if out is None else out[1])
-        _mx_quantize(x, row, col, tiled, scale_rule, seed, handle)
-        return row, col
-
-    return _on(dev, stream, body)
+    if not _here(dev, stream):
+        with _at(dev, stream):
+            return mxfp4_quantize_both(x, tiled, scale_rule, seed, out)
+    rows, cols = x.shape
+    row = _mx_view(rows, cols, tiled, dev, None if out is None else out[0])
+    col = _mx_view(cols, rows, tiled, dev, None if out is None else out[1])
+    _mx_quantize(x, row, col, tiled, scale_rule, seed)
+    return row, col
 
 
 def _mx_out(out, rows: int, cols: int, dtype, device):
@@ -312,15 +319,14 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols:
     """The values of a rows x cols MXFP4 matrix (fs4_mxfp4_dequantize) in `dtype`, or in `out`."""
     dev = codes.device
     _mx_check((codes, scales), rows, cols, tiled, "codes and scales", dev)
-
-    def body(handle):
-        y = _mx_out(out, rows, cols, dtype, dev)
-        check(_lib.lib().fs4_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, y.data_ptr(),
-                                              _DTYPES[y.dtype], _ld(y), FS4_LAYOUT_TILED if tiled else 0, handle),
-              "fs4_mxfp4_dequantize")
-        return y
-
-    return _on(dev, stream, body)
+    if not _here(dev, stream):
+        with _at(dev, stream):
+            return mxfp4_dequantize(codes, scales, rows, cols, tiled, dtype, out)
+    y = _mx_out(out, rows, cols, dtype, dev)
+    check(_lib.lib().fs4_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, y.data_ptr(), _DTYPES[y.dtype],
+                                          _ld(y), FS4_LAYOUT_TILED if tiled else 0, _handle(dev)),
+          "fs4_mxfp4_dequantize")
+    return y
 
 
 def mxfp4_gemm(a, b, M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
@@ -333,19 +339,19 @@ def mxfp4_gemm(a, b, M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16
     _mx_check(b, N, K, True, "b", dev)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    if workspace is not None:
+    if not _here(dev, stream):
+        with _at(dev, stream):
+            return mxfp4_gemm(a, b, M, N, K, dtype, out, accumulate, workspace)
+    d = _mx_out(out, M, N, dtype, dev)
+    if workspace is None:
+        workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+    else:
         _check_bytes(workspace, 256, "workspace", dev)
-
-    def body(handle):
-        d = _mx_out(out, M, N, dtype, dev)
-        ws = torch.zeros(256, dtype=torch.uint8, device=dev) if workspace is None else workspace
-        check(_lib.lib().fs4_mxfp4_gemm(a[0].data_ptr(), a[1].data_ptr(), b[0].data_ptr(), b[1].data_ptr(), M, N, K,
-                                        d.data_ptr(), _DTYPES[d.dtype], _ld(d),
-                                        _lib.FS4_MX_ACCUMULATE if accumulate else 0, ws.data_ptr(), ws.numel(), handle),
-              "fs4_mxfp4_gemm")
-        return d
-
-    return _on(dev, stream, body)
+    check(_lib.lib().fs4_mxfp4_gemm(a[0].data_ptr(), a[1].data_ptr(), b[0].data_ptr(), b[1].data_ptr(), M, N, K, d.data_ptr(),
+                                    _DTYPES[d.dtype], _ld(d), _lib.FS4_MX_ACCUMULATE if accumulate else 0,
+                                    workspace.data_ptr(), workspace.numel(), _handle(dev)),
+          "fs4_mxfp4_gemm")
+    return d
 
 
 def mxfp4_linear_workspace_size(M: int, K: int) -> int:
@@ -363,24 +369,22 @@ def mxfp4_linear(x: torch.Tensor, w, N: int, dtype: torch.dtype | None = None, s
     _mx_check(w, N, K, True, "w", dev)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    flags = _mx_scale_flag(scale_rule) | (_lib.FS4_MX_ACCUMULATE if accumulate else 0)
+    if not _here(dev, stream):
+        with _at(dev, stream):
+            return mxfp4_linear(x, w, N, dtype, scale_rule, out, accumulate, workspace)
+    d = _mx_out(out, M, N, x.dtype if dtype is None else dtype, dev)
     need = 256 + 17 * mxfp4_tiled_shape(M, K)[1]             # mxfp4_linear_workspace_size(M, K)
-    if workspace is not None:
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace[:256].zero_()
+    else:
         _check_bytes(workspace, need, "workspace", dev)
-
-    def body(handle):
-        d = _mx_out(out, M, N, x.dtype if dtype is None else dtype, dev)
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-            ws[:256].zero_()
-        check(_lib.lib().fs4_mxfp4_linear(x.data_ptr(), _DTYPES[x.dtype], M, K, _ld(x), w[0].data_ptr(),
-                                          w[1].data_ptr(), N, d.data_ptr(), _DTYPES[d.dtype], _ld(d), flags,
-                                          ws.data_ptr(), ws.numel(), handle),
-              "fs4_mxfp4_linear")
-        return d
-
-    return _on(dev, stream, body)
+    check(_lib.lib().fs4_mxfp4_linear(x.data_ptr(), _DTYPES[x.dtype], M, K, _ld(x), w[0].data_ptr(), w[1].data_ptr(), N,
+                                      d.data_ptr(), _DTYPES[d.dtype], _ld(d),
+                                      _mx_scale_flag(scale_rule) | (_lib.FS4_MX_ACCUMULATE if accumulate else 0),
+                                      workspace.data_ptr(), workspace.numel(), _handle(dev)),
+          "fs4_mxfp4_linear")
+    return d
 
 
 def muon_workspace_size(shapes: Sequence[tuple[int, int]]) -> int:
@@ -398,25 +402,25 @@ def _muon_coeffs(coeffs, K: int):
     return (ctypes.c_float * len(flat))(*flat), len(flat) // 3
 
 
-def _muon_call(ws_list, gs, ms, scales, K, coeffs, workspace, stream, step):
+def _muon_call(ws_list, gs, ms, scales, K, coeffs, workspace, step):
     n, dev = len(gs), gs[0].device
     arr = (_lib.MuonDesc * n)()
-    for i, (w, g) in enumerate(zip(ws_list, gs)):
-        m = ms[i] if ms is not None else None
-        arr[i] = _lib.MuonDesc(w.data_ptr(), g.data_ptr(), _ptr(m), g.shape[0], g.shape[1], _ld(w), _ld(g),
-                               0 if m is None else _ld(m), _DTYPES[w.dtype], _DTYPES[g.dtype],
-                               0 if m is None else _DTYPES[m.dtype], scales[i])
+    for d, w, g, m, scale in zip(arr, ws_list, gs, ms, scales):
+        d.w, d.g, d.scale = w.data_ptr(), g.data_ptr(), scale
+        d.rows, d.cols = g.shape
+        d.ld_w, d.ld_g, d.w_dtype, d.g_dtype = _ld(w), _ld(g), _DTYPES[w.dtype], _DTYPES[g.dtype]
+        if m is not None:
+            d.m, d.ld_m, d.m_dtype = m.data_ptr(), _ld(m), _DTYPES[m.dtype]
     c, nc = _muon_coeffs(coeffs, K)
-    need = muon_workspace_size([g.shape for g in gs])
-    if workspace is not None:
-        _check_bytes(workspace, need, "workspace", dev)
-    else:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(muon_workspace_size([g.shape for g in gs]), 1), dtype=torch.uint8, device=dev)
+    else:      # the call itself checks its size
+        _check_bytes(workspace, 1, "workspace", dev)
     if step is None:
-        check(_lib.lib().fs4_muon_orthogonalize(n, arr, K, c, nc, workspace.data_ptr(), workspace.numel(), stream),
+        check(_lib.lib().fs4_muon_orthogonalize(n, arr, K, c, nc, workspace.data_ptr(), workspace.numel(), _handle(dev)),
               "fs4_muon_orthogonalize")
     else:
-        check(_lib.lib().fs4_muon_step(n, arr, K, c, nc, *step, workspace.data_ptr(), workspace.numel(), stream),
+        check(_lib.lib().fs4_muon_step(n, arr, K, c, nc, *step, workspace.data_ptr(), workspace.numel(), _handle(dev)),
               "fs4_muon_step")
 
 
@@ -432,13 +436,12 @@ def muon_orthogonalize(Gs: Sequence[torch.Tensor], K: int = 5, coeffs=MUON_COEFF
         _check_matrix(G, f"Gs[{i}]", dev)
     if outs is not None and len(outs) != len(Gs):
         raise ValueError(f"{len(outs)} outs for {len(Gs)} matrices")
-
-    def body(handle):
-        res = [_mx_out(None if outs is None else outs[i], *G.shape, dtype, dev) for i, G in enumerate(Gs)]
-        _muon_call(res, Gs, None, [1.0] * len(Gs), K, coeffs, workspace, handle, None)
-        return res
-
-    return _on(dev, stream, body)
+    if not _here(dev, stream):
+        with _at(dev, stream):
+            return muon_orthogonalize(Gs, K, coeffs, dtype, outs, workspace)
+    outs = [_mx_out(None if outs is None else outs[i], *G.shape, dtype, dev) for i, G in enumerate(Gs)]
+    _muon_call(outs, Gs, [None] * len(Gs), [1.0] * len(Gs), K, coeffs, workspace, None)
+    return outs
 
 
 def _muon_scale(scale, rows: int, cols: int) -> float:
@@ -466,9 +469,11 @@ def muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], mom
             _check_matrix(t, f"{name}[{i}]", dev)
             if t.shape != ts[0].shape:
                 raise ValueError(f"{name}[{i}] must have the shape of params[{i}], {tuple(ts[0].shape)}")
-    scales = [_muon_scale(scale, *p.shape) for p in params]
-    extra = (lr, beta, weight_decay, _lib.FS4_MUON_NESTEROV if nesterov else 0)
-    _on(dev, stream, lambda handle: _muon_call(params, grads, momenta, scales, K, coeffs, workspace, handle, extra))
+    if not _here(dev, stream):
+        with _at(dev, stream):
+            return muon_step(params, grads, momenta, lr, beta, nesterov, weight_decay, K, coeffs, scale, workspace)
+    _muon_call(params, grads, momenta, [_muon_scale(scale, *p.shape) for p in params], K, coeffs, workspace,
+               (lr, beta, weight_decay, _lib.FS4_MUON_NESTEROV if nesterov else 0))
 
 
 def _ld(t: torch.Tensor) -> int:

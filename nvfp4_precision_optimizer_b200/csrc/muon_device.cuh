@@ -23,6 +23,9 @@ __device__ __forceinline__ float get1(const void* p, int64_t i, int type) {
   if (type == kTypeBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
   return __half2float(static_cast<const __half*>(p)[i]);
 }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 // Round to the type and back: what a later read sees.
 __device__ __forceinline__ float put1(void* p, int64_t i, int type, float v) {
   if (type == kTypeF32) {

@@ -20,32 +20,78 @@ namespace {
 constexpr int kThreads = 256;
 static_assert(kMuonChunk == kThreads, "one column a thread");
 
-// U's columns c0 .. c0 + 255 into u[row][column].
-__device__ __forceinline__ void load_chunk(const MuonCall& p, const MuonMat& d, int64_t c0, float (*u)[kMuonChunk + 1]) {
-  const int count = d.m * kMuonChunk;
-  for (int i = threadIdx.x; i < count; i += kThreads) {
-    // neighbouring threads read neighbouring elements of G
-    const int r = d.tall ? i % d.m : i / kMuonChunk, c = d.tall ? i / d.m : i % kMuonChunk;
-    float v = 0.0f;
-    if (c0 + c < d.n) v = d.tall ? direction_at(p, d, c0 + c, r) : direction_at(p, d, r, c0 + c);
-    u[r][c] = v;
-  }
+// Rows r0 .. r0 + 7 of array element column c of an m x n working matrix (tall: stored n x m);
+// absent ones are 0.  The eight loads are in flight together.
+template <typename T>
+__device__ __forceinline__ void column8(const void* p, int64_t ld, const MuonMat& d, int r0, int64_t c, float* v) {
+  const T* q = static_cast<const T*>(p);
+  T raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (r0 + i < d.m && c < d.n) raw[i] = d.tall ? q[c * ld + r0 + i] : q[(int64_t)(r0 + i) * ld + c];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = (r0 + i < d.m && c < d.n) ? to_f32(raw[i]) : 0.0f;
+}
+__device__ __forceinline__ void column8_of(const void* p, int64_t ld, int type, const MuonMat& d, int r0, int64_t c, float* v) {
+  if (type == kTypeF32) column8<float>(p, ld, d, r0, c, v);
+  else if (type == kTypeBf16) column8<__nv_bfloat16>(p, ld, d, r0, c, v);
+  else column8<__half>(p, ld, d, r0, c, v);
+}
+// The same of U.
+__device__ __forceinline__ void direction_column8(const MuonCall& p, const MuonMat& d, int r0, int64_t c, float* v) {
+  column8_of(d.g, d.ldg, d.tg, d, r0, c, v);
+  if (!d.mom) return;
+  float m[8];
+  column8_of(d.mom, d.ldm, d.tm, d, r0, c, m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = direction(p, m[i], v[i]);
 }
 
+// Entries in 2 x 2 blocks on and above the diagonal; the threads left over by few blocks share
+// the columns.
 __global__ void __launch_bounds__(kThreads) muon_thin_gram_kernel(const __grid_constant__ MuonCall p) {
   __shared__ float u[kMuonThin][kMuonChunk + 1];
+  __shared__ double sums[kThreads][4];
   const MuonTable& t = *muon_table(p.ws);
   const int mi = owner_of(t.prefix[kUnitsThin], p.count, blockIdx.x);
   const MuonMat& d = t.mat[mi];
   const int32_t chunk = blockIdx.x - t.prefix[kUnitsThin][mi];
-  load_chunk(p, d, (int64_t)chunk * kMuonChunk, u);
+  const int m = d.m, mb = (m + 1) / 2, blocks = mb * (mb + 1) / 2, shares = kThreads / blocks;
+  for (int r = 0; r < m; r += 8) {
+    float v[8];
+    direction_column8(p, d, r, (int64_t)chunk * kMuonChunk + threadIdx.x, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[r + i][threadIdx.x] = v[i];      // rows past m are 0
+  }
   __syncthreads();
-  double* out = reinterpret_cast<double*>(p.ws + d.base + thin_gram_offset(d.m)) + (int64_t)chunk * d.m * d.m;
-  for (int e = threadIdx.x; e < d.m * d.m; e += kThreads) {
-    const int i = e / d.m, j = e % d.m;
-    double s = 0.0;
-    for (int c = 0; c < kMuonChunk; ++c) s += (double)u[i][c] * (double)u[j][c];
-    out[e] = s;
+  const int block = threadIdx.x % blocks, share = threadIdx.x / blocks;
+  int j = 0, i = block;                       // block (i, j), i <= j
+  while (i > j) i -= ++j;
+  if (share < shares) {
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int c = share; c < kMuonChunk; c += shares) {
+      const double a0 = u[2 * i][c], a1 = u[2 * i + 1][c], b0 = u[2 * j][c], b1 = u[2 * j + 1][c];
+      s[0] += a0 * b0;
+      s[1] += a0 * b1;
+      s[2] += a1 * b0;
+      s[3] += a1 * b1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sums[threadIdx.x][k] = s[k];
+  }
+  __syncthreads();
+  double* out = reinterpret_cast<double*>(p.ws + d.base + thin_gram_offset(m)) + (int64_t)chunk * m * m;
+  if (threadIdx.x < blocks) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      double s = 0.0;
+      for (int h = 0; h < shares; ++h) s += sums[h * blocks + threadIdx.x][k];
+      const int r = 2 * i + (k >> 1), c = 2 * j + (k & 1);
+      if (r < m && c < m) {
+        out[r * m + c] = s;
+        out[c * m + r] = s;
+      }
+    }
   }
 }
 
@@ -77,9 +123,15 @@ __global__ void __launch_bounds__(1024) muon_thin_iterate_kernel(const __grid_co
   __syncthreads();
   // one product: row i of x times column j of y
   auto dot = [&](const double (*x)[kMuonThin + 1], const double (*y)[kMuonThin + 1]) -> double {
-    double s = 0.0;
-    for (int t = 0; t < m; ++t) s += x[i][t] * y[t][j];
-    return s;
+    double s = 0.0, r = 0.0;          // two chains
+    int t = 0;
+#pragma unroll 4
+    for (; t + 1 < m; t += 2) {
+      s += x[i][t] * y[t][j];
+      r += x[i][t + 1] * y[t + 1][j];
+    }
+    if (t < m) s += x[i][t] * y[t][j];
+    return s + r;
   };
   for (int it = 0; it < p.K; ++it) {
     const float* c = p.coeffs + (p.n_coeffs == 1 ? 0 : 3 * it);
@@ -104,39 +156,58 @@ __global__ void __launch_bounds__(1024) muon_thin_iterate_kernel(const __grid_co
   }
 }
 
+// One column of X_K a thread: T U, T's rows read by all threads at once.
 __global__ void __launch_bounds__(kThreads) muon_thin_apply_kernel(const __grid_constant__ MuonCall p) {
-  __shared__ float u[kMuonThin][kMuonChunk + 1];
-  __shared__ float T[kMuonThin][kMuonThin];
+  __shared__ __align__(16) float T[kMuonThin][kMuonThin];
   const MuonTable& t = *muon_table(p.ws);
   const int mi = owner_of(t.prefix[kUnitsThin], p.count, blockIdx.x);
   const MuonMat& d = t.mat[mi];
-  const int64_t c0 = (int64_t)(blockIdx.x - t.prefix[kUnitsThin][mi]) * kMuonChunk;
+  const int64_t c = (int64_t)(blockIdx.x - t.prefix[kUnitsThin][mi]) * kMuonChunk + threadIdx.x;
+  const int m = d.m;
   const uint8_t* ws = p.ws + d.base;
-  const bool fine = *reinterpret_cast<const float*>(ws + thin_flag_offset(d.m)) != 0.0f;
-  for (int e = threadIdx.x; e < d.m * d.m; e += kThreads) T[e / d.m][e % d.m] = reinterpret_cast<const float*>(ws)[e];
-  load_chunk(p, d, c0, u);
-  __syncthreads();
-  // X_K of this thread's column, in place of U's
-  float x[kMuonThin];
-#pragma unroll
-  for (int i = 0; i < kMuonThin; ++i) {
-    if (i >= d.m) break;
-    float s = 0.0f;
-    for (int j = 0; j < d.m; ++j) s = fmaf(T[i][j], u[j][threadIdx.x], s);
-    x[i] = s;
+  for (int e = threadIdx.x; e < kMuonThin * kMuonThin; e += kThreads) {
+    const int i = e / kMuonThin, j = e % kMuonThin;
+    T[i][j] = (i < m && j < m) ? reinterpret_cast<const float*>(ws)[i * m + j] : 0.0f;
   }
+  const bool fine = *reinterpret_cast<const float*>(ws + thin_flag_offset(m)) != 0.0f;
+  float u[kMuonThin];
 #pragma unroll
-  for (int i = 0; i < kMuonThin; ++i)
-    if (i < d.m) u[i][threadIdx.x] = x[i];
+  for (int r = 0; r < kMuonThin; r += 8) {
+    if (r < m) {
+      direction_column8(p, d, r, c, u + r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[r + i] = 0.0f;
+    }
+  }
   __syncthreads();
+  if (c >= d.n) return;
+  const bool blend = p.rate >= 0.0f;
   bool bad = false;
-  for (int i = threadIdx.x; i < d.m * kMuonChunk; i += kThreads) {
-    const int r = d.tall ? i % d.m : i / kMuonChunk, c = d.tall ? i / d.m : i % kMuonChunk;
-    if (c0 + c >= d.n) continue;
-    const float v = fine ? u[r][c] * d.scale : 0.0f;
-    bad |= !isfinite(v);
-    const int64_t at = d.tall ? (c0 + c) * d.ldw + r : r * d.ldw + c0 + c;
-    put1(d.w, at, d.tw, p.rate < 0.0f ? v : fmaf(-p.rate, v, p.keep * get1(d.w, at, d.tw)));
+  for (int i0 = 0; i0 < m; i0 += 8) {
+    float w[8], s[8];
+    if (blend) column8_of(d.w, d.ldw, d.tw, d, i0, c, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kMuonThin; j += 4) {
+        if (j >= m) break;
+        const float4 q = *reinterpret_cast<const float4*>(&T[i0 + i][j]);
+        s[i] = fmaf(q.x, u[j], s[i]);
+        s[i] = fmaf(q.y, u[j + 1], s[i]);
+        s[i] = fmaf(q.z, u[j + 2], s[i]);
+        s[i] = fmaf(q.w, u[j + 3], s[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i0 + i >= m) break;
+      const float v = fine ? s[i] * d.scale : 0.0f;
+      bad |= !isfinite(v);
+      const int64_t at = d.tall ? c * d.ldw + i0 + i : (int64_t)(i0 + i) * d.ldw + c;
+      put1(d.w, at, d.tw, blend ? fmaf(-p.rate, v, p.keep * w[i]) : v);
+    }
   }
   if (bad) atomicOr(muon_status(p.ws), kStatusNonFinite);
 }

@@ -191,7 +191,7 @@ def test_refusals_on_device(fs4):
         fs4.muon_orthogonalize([G], outs=[torch.zeros(8, 15, device="cuda")])
     with pytest.raises(ValueError):
         fs4.muon_step([W], [G[:, :8]], [torch.zeros(8, 16, device="cuda")], 0.1)
-    with pytest.raises(ValueError):
+    with pytest.raises(fs4.Fs4Error):
         fs4.muon_orthogonalize([G], workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(fs4.Fs4Error):
         fs4.muon_step([W], [G], [W], 0.1)                      # momentum and weights in one place
