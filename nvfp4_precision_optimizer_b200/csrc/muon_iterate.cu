@@ -161,9 +161,9 @@ __device__ __forceinline__ Job make_job(const MuonCall& p, const Shared& sh, int
   return j;
 }
 
-// Whether the 256-block of row (or column) `at` of a symmetric operand at k step `k` is read as
-// its mirror image.
-__device__ __forceinline__ bool mirrored(int32_t at, int32_t k) { return (k >> 2) < (at >> 8); }
+// Row `at` of a symmetric operand is stored from the 256-block on the diagonal on: the first k
+// step there.  Steps before it are read as the mirror image.
+__device__ __forceinline__ int32_t first_row_step(int32_t at) { return (at >> 8) * 4; }
 
 struct Maps {
   CUtensorMap rows128, rows64;     // the workspace as 128-byte rows, copied 128 or 64 at a time
@@ -181,18 +181,31 @@ __device__ __forceinline__ void copy_rows(const Target& t, uint32_t dst, int64_t
   if constexpr (kPair) tma_rows_pair(dst, kRows == 128 ? &t.maps->rows128 : &t.maps->rows64, (int32_t)(src >> 7), t.cluster_bar);
   else bulk_g2s_addr(dst, t.ws + src, 128 * kRows, t.bar);
 }
-// kRows (64 or 128) rows of M or N from row0 on, 64 k: a tile or half of one.
+// One operand of a job: kRows (64 or 128) of its rows of M or N, 64 k at a time.  Addresses advance
+// by constants; the producer's thread has little time for more.
 template <bool kPair, int kRows>
-__device__ __forceinline__ void load_rows(const Target& t, uint32_t dst, int64_t src, int32_t cp, int32_t row0, int32_t k) {
-  copy_rows<kPair, kRows>(t, dst, src + ((int64_t)(row0 >> 7) * (cp >> 6) + k) * kTileBytes16 + (row0 & 127) * 128);
-}
-// 64 stored rows from 64 k on, kCols (64 or 128) columns from col0 on: halves of neighbouring tiles.
-template <bool kPair, int kCols>
-__device__ __forceinline__ void load_columns(const Target& t, uint32_t dst, int64_t src, int32_t cp, int32_t col0, int32_t k) {
-  const int64_t at = src + ((int64_t)(k >> 1) * (cp >> 6) + (col0 >> 6)) * kTileBytes16 + (k & 1) * (kTileBytes16 / 2);
+struct Source {
+  int64_t rows, columns;     // k step 0, read by rows (a tile, or half of one, per step) ...
+  int64_t pitch;             // ... or, mirrored, by columns: 128 stored rows are `pitch` apart
+  int32_t turn;              // k steps below this are read by columns
+
+  // rows at.. of a matrix with cp padded columns at src
+  __device__ __forceinline__ Source(int64_t src, int32_t cp, int32_t at, int32_t turn_) : turn(turn_) {
+    pitch = (int64_t)(cp >> 6) * kTileBytes16;
+    rows = src + (at >> 7) * pitch + (at & 127) * 128;
+    columns = src + (int64_t)(at >> 6) * kTileBytes16;
+  }
+  __device__ __forceinline__ void copy(const Target& t, uint32_t dst, int32_t k) const {
+    if (k < turn) {
+      // 64 stored rows, halves of neighbouring tiles
+      const int64_t from = columns + (k >> 1) * pitch + (k & 1) * (kTileBytes16 / 2);
 #pragma unroll
-  for (int i = 0; i < kCols / 64; ++i) copy_rows<kPair, 64>(t, dst + i * (kTileBytes16 / 2), at + i * kTileBytes16);
-}
+      for (int i = 0; i < kRows / 64; ++i) copy_rows<kPair, 64>(t, dst + i * (kTileBytes16 / 2), from + i * kTileBytes16);
+    } else {
+      copy_rows<kPair, kRows>(t, dst, rows + (int64_t)k * kTileBytes16);
+    }
+  }
+};
 
 // ------------------------------------------------------------------ epilogue
 // Chunks 2 i and 2 i + 1 of a row lie in one 32-byte piece, in the order of the row's bit 0.
@@ -209,8 +222,7 @@ __device__ __forceinline__ uint4 quad(const Pair& p, int i) { return make_uint4(
 
 // 32 results (columns col .. col + 31 of working row `row`) into the weights or the output.
 template <typename T>
-__device__ __forceinline__ void write_result(const MuonCall& p, const MuonMat& d, int32_t row, int32_t col, const float* y, bool& bad) {
-  if (row >= d.m) return;
+__device__ __forceinline__ void write_result(const MuonCall& p, const MuonMat& d, int32_t row, int32_t col, float* y, int lane, bool& bad) {
   constexpr int kPer = 32 / (int)sizeof(T);                  // elements of 32 bytes
   const bool blend = p.rate >= 0.0f;
   auto result = [&](float x, float w) -> float {
@@ -220,6 +232,7 @@ __device__ __forceinline__ void write_result(const MuonCall& p, const MuonMat& d
   };
   T* w = static_cast<T*>(d.w);
   if (!d.tall && col + 32 <= d.n && ((reinterpret_cast<uintptr_t>(w) | (uintptr_t)(d.ldw * (int64_t)sizeof(T))) & 31) == 0) {
+    if (row >= d.m) return;
     T* at = w + row * d.ldw + col;
 #pragma unroll
     for (int q = 0; q < 32 / kPer; ++q) {
@@ -236,11 +249,34 @@ __device__ __forceinline__ void write_result(const MuonCall& p, const MuonMat& d
     }
     return;
   }
+  if (d.tall) {               // neighbouring lanes hold neighbouring elements
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (col + i >= d.n || row >= d.m) break;
+      T* at = w + (int64_t)(col + i) * d.ldw + row;
+      put_as(at, result(y[i], blend ? get_as(at) : 0.0f));
+    }
+    return;
+  }
+  // rows that do not start on 32 bytes: the warp's 32 x 32 values change places (lane and
+  // register), then a row at a time
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i & s) continue;
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, (lane & s) ? y[i] : y[i + s], s);
+      if (lane & s) y[i] = got;
+      else y[i + s] = got;
+    }
+  }
+  const int32_t r0 = row - lane;
+  if (col + lane >= d.n) return;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    if (col + i >= d.n) break;
-    const int64_t at = d.tall ? (int64_t)(col + i) * d.ldw + row : row * d.ldw + col + i;
-    put_as(w + at, result(y[i], blend ? get_as(w + at) : 0.0f));
+    if (r0 + i >= d.m) break;
+    T* at = w + (int64_t)(r0 + i) * d.ldw + col + lane;
+    put_as(at, result(y[i], blend ? get_as(at) : 0.0f));
   }
 }
 
@@ -341,12 +377,13 @@ __device__ __forceinline__ void epilogue(const MuonCall& p, const Place<kPair, E
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= kAScale / (kXScale * kXScale);
       if (on) {
+        float e = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (lane == i) {
-            w.da[w.row] = v[i] * (1.0f / kAScale);
-            v[i] = 0.0f;
-          }
+        for (int i = 0; i < 32; ++i) {
+          e = lane == i ? v[i] : e;
+          v[i] = lane == i ? 0.0f : v[i];
+        }
+        w.da[w.row] = e * (1.0f / kAScale);
       }
     } else {
       const Input in = a.in[0];
@@ -387,9 +424,9 @@ __device__ __forceinline__ void epilogue(const MuonCall& p, const Place<kPair, E
     if (last) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= 1.0f / kXScale;
-      if (m->tw == kTypeF32) write_result<float>(p, *m, w.row, col, v, bad);
-      else if (m->tw == kTypeBf16) write_result<__nv_bfloat16>(p, *m, w.row, col, v, bad);
-      else write_result<__half>(p, *m, w.row, col, v, bad);
+      if (m->tw == kTypeF32) write_result<float>(p, *m, w.row, col, v, lane, bad);
+      else if (m->tw == kTypeBf16) write_result<__nv_bfloat16>(p, *m, w.row, col, v, lane, bad);
+      else write_result<__half>(p, *m, w.row, col, v, lane, bad);
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -447,6 +484,7 @@ __device__ __forceinline__ bool produce(const MuonCall& p, const Maps& maps, Sha
                                         uint32_t rank, volatile int* abort) {
   using T = Tile<kPair>;
   const int32_t total = sh.prefix[E][p.count];
+  const uint32_t leader_full = kPair ? cluster_map(smem_addr(&sh.full[0]), 0) : 0u;
   for (int32_t u = first_unit<kPair>(); u < total; u += unit_step<kPair>()) {
     const Job j = make_job<kPair, E>(p, sh, u, rank);
     const Block& d = sh.block[j.mat];
@@ -454,24 +492,19 @@ __device__ __forceinline__ bool produce(const MuonCall& p, const Maps& maps, Sha
     const MuonLayout L = muon_layout(mp, np);
     const int64_t x = d.base + ((it & 1) ? L.x[1] : L.x[0]);
     const int64_t sym = d.base + (E == kSquare ? L.a : L.b);
-    for (int32_t i = 0; i < j.steps; ++i) {
-      const int32_t k = j.k0 + i;
+    // symmetric operands are read as their mirror image below the diagonal's 256-blocks; X as
+    // the update's second operand always by columns
+    const Source<kPair, 128> first(E == kGram ? x : sym, E == kGram ? np : mp, j.row0, E == kGram ? 0 : first_row_step(j.row0));
+    const Source<kPair, T::kB / 128> second(E == kSquare ? sym : x, E == kSquare ? mp : np, j.n0,
+                                            E == kGram ? 0 : E == kSquare ? first_row_step(j.n0) : 0x7FFFFFFF);
+    for (int32_t k = j.k0; k < j.k0 + j.steps; ++k) {
       if (!mbar_wait(&sh.empty[ring.s], ring.ph ^ 1u, muon_status(p.ws), abort)) return false;
-      const uint32_t a = base + ring.s * T::kStage, b = a + T::kA;
+      const uint32_t a = base + ring.s * T::kStage;
       Target t{&maps, p.ws, &sh.full[ring.s], 0u};
-      if constexpr (kPair) t.cluster_bar = cluster_map(smem_addr(&sh.full[ring.s]), 0);
+      if constexpr (kPair) t.cluster_bar = leader_full + 8 * ring.s;
       if (rank == 0) mbar_arrive_expect_tx(&sh.full[ring.s], (kPair ? 2 : 1) * T::kStage);
-      constexpr int kBRows = T::kB / 128;
-      if constexpr (E == kGram) {
-        load_rows<kPair, 128>(t, a, x, np, j.row0, k);
-        load_rows<kPair, kBRows>(t, b, x, np, j.n0, k);
-      } else {
-        if (mirrored(j.row0, k)) load_columns<kPair, 128>(t, a, sym, mp, j.row0, k);
-        else load_rows<kPair, 128>(t, a, sym, mp, j.row0, k);
-        if constexpr (E == kUpdate) load_columns<kPair, kBRows>(t, b, x, np, j.n0, k);
-        else if (mirrored(j.n0, k)) load_columns<kPair, kBRows>(t, b, sym, mp, j.n0, k);
-        else load_rows<kPair, kBRows>(t, b, sym, mp, j.n0, k);
-      }
+      first.copy(t, a, k);
+      second.copy(t, a + T::kA, k);
       ring.next();
     }
   }
@@ -491,12 +524,15 @@ __device__ __forceinline__ bool multiply(const MuonCall& p, Shared& sh, Ring<kPa
     const uint32_t acc = tmem + (uint32_t)T::kN * (tl & 1u);
     if (!mbar_wait_cluster(&sh.acc_empty[tl & 1u], ((tl >> 1) & 1u) ^ 1u, muon_status(p.ws), abort)) return false;
     tc_fence_after();
+    const int32_t a_turn = E == kGram ? 0 : first_row_step(j.row0);
+    const int32_t b_turn = E == kGram ? 0 : E == kSquare ? first_row_step(j.n0) : 0x7FFFFFFF;
     for (int32_t i = 0; i < j.steps; ++i) {
       const int32_t k = j.k0 + i;
-      if (!mbar_wait_cluster(&sh.full[ring.s], ring.ph, muon_status(p.ws), abort)) return false;
+      const bool landed = kPair ? mbar_wait_cluster(&sh.full[ring.s], ring.ph, muon_status(p.ws), abort)
+                                : mbar_wait(&sh.full[ring.s], ring.ph, muon_status(p.ws), abort);
+      if (!landed) return false;
       tc_fence_after();
-      const bool am = E != kGram && mirrored(j.row0, k);
-      const bool bm = E == kUpdate || (E == kSquare && mirrored(j.n0, k));
+      const bool am = k < a_turn, bm = k < b_turn;
       // 16 k: 32 bytes along a row, or 16 rows of 128 bytes
       const uint64_t da = (am ? ca0 : ra0) + ring.s * kStep, db = (bm ? cb0 : rb0) + ring.s * kStep;
       const uint64_t ia = am ? 128 : 2, ib = bm ? 128 : 2;
@@ -706,7 +742,6 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
       // a producer that sees the count fences its TMA copies behind it
       named_bar(1, 256);
       if (threadIdx.x == 64) {
-        __threadfence();
         asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(muon_barrier(p.ws)), "r"(1u) : "memory");
       }
     }
