@@ -58,10 +58,8 @@ __global__ void __launch_bounds__(kThreads, 2) muon_moment_kernel(const __grid_c
       out->prefix[i / (p.count + 1)][i % (p.count + 1)] = t.prefix[i / (p.count + 1)][i % (p.count + 1)];
     for (int i = threadIdx.x; i < p.count; i += kThreads) out->mat[i] = t.mat[i];
     for (int i = threadIdx.x; i < p.counts; i += kThreads) reinterpret_cast<uint32_t*>(p.ws + p.counts_at)[i] = 0u;
-    if (threadIdx.x == 0) {
-      *muon_status(p.ws) = 0u;
-      *muon_barrier(p.ws) = 0u;
-    }
+    for (int i = threadIdx.x; i < p.count; i += kThreads) muon_counts(p.ws)[i] = 0u;
+    if (threadIdx.x == 0) *muon_status(p.ws) = 0u;
   }
   const int32_t u = blockIdx.x;
   if (u >= t.prefix[kUnitsMoment][p.count]) return;

@@ -65,13 +65,14 @@ struct MuonCall {
   float coeffs[3 * FS4_MAX_ITERS];
 };
 
-// Workspace: [header | table | partial sums | one block per matrix].  Header: the status word at
-// byte 0, the iterate kernel's barrier count at byte 128.
-constexpr int64_t kMuonHeader = 256, kMuonBarrier = 128;
-constexpr int64_t kMuonPartials = (kMuonHeader + (int64_t)sizeof(MuonTable) + 255) / 256 * 256;
+// Workspace: [header | counts | table | partial sums | one block per matrix].  Header: the status
+// word at byte 0.  Counts: the iterate kernel's finished work, a word per matrix.
+constexpr int64_t kMuonHeader = 256, kMuonTableAt = kMuonHeader + 4 * kMuonMaxBatch;
+static_assert(kMuonTableAt % 16 == 0, "the table holds pointers");
+constexpr int64_t kMuonPartials = (kMuonTableAt + (int64_t)sizeof(MuonTable) + 255) / 256 * 256;
 __host__ __device__ inline uint32_t* muon_status(uint8_t* ws) { return reinterpret_cast<uint32_t*>(ws); }
-__host__ __device__ inline uint32_t* muon_barrier(uint8_t* ws) { return reinterpret_cast<uint32_t*>(ws + kMuonBarrier); }
-__host__ __device__ inline MuonTable* muon_table(uint8_t* ws) { return reinterpret_cast<MuonTable*>(ws + kMuonHeader); }
+__host__ __device__ inline uint32_t* muon_counts(uint8_t* ws) { return reinterpret_cast<uint32_t*>(ws + kMuonHeader); }
+__host__ __device__ inline MuonTable* muon_table(uint8_t* ws) { return reinterpret_cast<MuonTable*>(ws + kMuonTableAt); }
 __host__ __device__ inline double* muon_partials(uint8_t* ws) { return reinterpret_cast<double*>(ws + kMuonPartials); }
 
 // Small calls of the iterate kernel: tiles of 128 rows x 64 columns, only those that hold rows and

@@ -24,9 +24,11 @@
 // epilogue each, only over the rows and columns that the matrices have; a long Gram product is
 // split along K, the partial tiles summed in order by the CTA that finishes last.  Two accumulators: a block's epilogue overlaps the
 // next block's MMAs.  Both CTAs' copies count on the leader's barrier (tensor maps allow that);
-// a relay through the other CTA's threads took 1300 cycles a stage.  Between products the
-// launch's CTAs meet at a counter in the workspace (a cooperative launch: all are resident; the
-// wait is bounded), which saves 3K - 1 launches and their set-up.
+// a relay through the other CTA's threads took 1300 cycles a stage.  The units of all products form one
+// sequence, dealt to the CTAs in turn; a unit waits until its matrix's product before is complete (a
+// count per matrix in the workspace; the waits are bounded), so the tail of one matrix's product
+// overlaps another's, and 3K - 1 launches and their set-up are saved.  Nothing waits for a later
+// unit, and all CTAs are resident (a cooperative launch), so some unit can always go on.
 #include <cstdint>
 #include <cstddef>
 #include <type_traits>
@@ -63,7 +65,6 @@ struct Shared {
   uint64_t empty[8];           // the MMAs reading the stage finished (both CTAs)
   uint64_t acc_full[2];
   uint64_t acc_empty[2];       // (leader) the accumulator is drained
-  uint64_t go;                 // the producer saw every CTA finish the product before
   uint64_t done;
   uint32_t tmem;
   int32_t abort;
@@ -168,6 +169,28 @@ __device__ __forceinline__ int32_t first_row_step(int32_t at) { return (at >> 8)
 struct Maps {
   CUtensorMap rows128, rows64;     // the workspace as 128-byte rows, copied 128 or 64 at a time
 };
+
+// The units of product number ph (0 .. 3K - 1) that this CTA or pair takes: dealt on from where the
+// product before ended.
+template <bool kPair>
+struct Deal {
+  int32_t next = kPair ? blockIdx.x >> 1 : blockIdx.x;
+  __device__ __forceinline__ int32_t step() const { return kPair ? gridDim.x >> 1 : gridDim.x; }
+  // after a product of `total` units
+  __device__ __forceinline__ void skip(int32_t total) {
+    next = (next - total) % step();
+    if (next < 0) next += step();
+  }
+};
+
+// What a matrix's count must have reached before its units of product (it, E) start: every epilogue
+// warp adds one when its part of a unit is stored.
+template <bool kPair, int E>
+__device__ __forceinline__ uint32_t units_before(const Shared& sh, int mat, int it) {
+  const int32_t g = sh.prefix[kGram][mat + 1] - sh.prefix[kGram][mat], q = sh.prefix[kSquare][mat + 1] - sh.prefix[kSquare][mat],
+                x = sh.prefix[kUpdate][mat + 1] - sh.prefix[kUpdate][mat];
+  return (uint32_t)(it * (g + q + x) + (E > kGram ? g : 0) + (E > kSquare ? q : 0)) * (kPair ? 16u : 8u);
+}
 
 // Where a CTA's copies go and are counted.
 struct Target {
@@ -442,7 +465,7 @@ __device__ __forceinline__ void epilogue(const MuonCall& p, const Place<kPair, E
   if (bad) atomicOr(muon_status(p.ws), kStatusNonFinite);
 }
 
-// ------------------------------------------------------------------ the launch's barrier
+// ------------------------------------------------------------------ counts in the workspace
 __device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
   uint32_t v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -473,25 +496,26 @@ struct Ring {
     if (++s == (uint32_t)Tile<kPair>::kStages) { s = 0; ph ^= 1u; }
   }
 };
-// Units are dealt to CTA pairs or CTAs in turn.
-template <bool kPair>
-__device__ __forceinline__ int32_t first_unit() { return kPair ? blockIdx.x >> 1 : blockIdx.x; }
-template <bool kPair>
-__device__ __forceinline__ int32_t unit_step() { return kPair ? gridDim.x >> 1 : gridDim.x; }
 
 template <bool kPair, int E>
-__device__ __forceinline__ bool produce(const MuonCall& p, const Maps& maps, Shared& sh, Ring<kPair>& ring, int it, uint32_t base,
+__device__ __forceinline__ bool produce(const MuonCall& p, const Maps& maps, Shared& sh, Ring<kPair>& ring, Deal<kPair>& deal, int it, uint32_t base,
                                         uint32_t rank, volatile int* abort) {
   using T = Tile<kPair>;
   const int32_t total = sh.prefix[E][p.count];
   const uint32_t leader_full = kPair ? cluster_map(smem_addr(&sh.full[0]), 0) : 0u;
-  for (int32_t u = first_unit<kPair>(); u < total; u += unit_step<kPair>()) {
+  int seen = -1;       // the last matrix found ready for this product
+  for (int32_t u = deal.next; u < total; u += deal.step()) {
     const Job j = make_job<kPair, E>(p, sh, u, rank);
     const Block& d = sh.block[j.mat];
     const int32_t mp = padded(d.m), np = padded(d.n);
     const MuonLayout L = muon_layout(mp, np);
     const int64_t x = d.base + ((it & 1) ? L.x[1] : L.x[0]);
     const int64_t sym = d.base + (E == kSquare ? L.a : L.b);
+    if (j.mat != seen && (E != kGram || it > 0)) {
+      if (!wait_count(muon_counts(p.ws) + j.mat, units_before<kPair, E>(sh, j.mat, it), muon_status(p.ws), abort)) return false;
+      fence_async();
+      seen = j.mat;
+    }
     // symmetric operands are read as their mirror image below the diagonal's 256-blocks; X as
     // the update's second operand always by columns
     const Source<kPair, 128> first(E == kGram ? x : sym, E == kGram ? np : mp, j.row0, E == kGram ? 0 : first_row_step(j.row0));
@@ -508,18 +532,19 @@ __device__ __forceinline__ bool produce(const MuonCall& p, const Maps& maps, Sha
       ring.next();
     }
   }
+  deal.skip(total);
   return true;
 }
 
 template <bool kPair, int E>
-__device__ __forceinline__ bool multiply(const MuonCall& p, Shared& sh, Ring<kPair>& ring, uint32_t& tl, uint32_t base, uint32_t tmem,
+__device__ __forceinline__ bool multiply(const MuonCall& p, Shared& sh, Ring<kPair>& ring, Deal<kPair>& deal, uint32_t& tl, uint32_t base, uint32_t tmem,
                                          volatile int* abort) {
   using T = Tile<kPair>;
   const uint64_t ra0 = sdesc_sw128(base), rb0 = sdesc_sw128(base + T::kA);
   const uint64_t ca0 = sdesc_sw128_mn(base, kTileBytes16 / 2), cb0 = sdesc_sw128_mn(base + T::kA, kTileBytes16 / 2);
   constexpr uint64_t kStep = T::kStage >> 4;
   const int32_t total = sh.prefix[E][p.count];
-  for (int32_t u = first_unit<kPair>(); u < total; u += unit_step<kPair>(), ++tl) {
+  for (int32_t u = deal.next; u < total; u += deal.step(), ++tl) {
     const Job j = make_job<kPair, E>(p, sh, u, 0);
     const uint32_t acc = tmem + (uint32_t)T::kN * (tl & 1u);
     if (!mbar_wait_cluster(&sh.acc_empty[tl & 1u], ((tl >> 1) & 1u) ^ 1u, muon_status(p.ws), abort)) return false;
@@ -549,6 +574,7 @@ __device__ __forceinline__ bool multiply(const MuonCall& p, Shared& sh, Ring<kPa
     if constexpr (kPair) tc_commit_pair(&sh.acc_full[tl & 1u]);
     else tc_commit(&sh.acc_full[tl & 1u]);
   }
+  deal.skip(total);
   return true;
 }
 
@@ -593,19 +619,28 @@ __device__ __forceinline__ bool sum_parts(const MuonCall& p, Shared& sh, const J
 }
 
 template <bool kPair, int E>
-__device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, uint32_t& tl, int it, uint32_t tmem, uint32_t rank, int quad_,
+__device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, Deal<kPair>& deal, uint32_t& tl, int it, uint32_t tmem, uint32_t rank, int quad_,
                                        int half, int lane, volatile int* abort) {
   using T = Tile<kPair>;
   const int32_t total = sh.prefix[E][p.count];
-  for (int32_t u = first_unit<kPair>(); u < total; u += unit_step<kPair>(), ++tl) {
+  int seen = -1;
+  for (int32_t u = deal.next; u < total; u += deal.step(), ++tl) {
     const Job j = make_job<kPair, E>(p, sh, u, rank);
     const uint32_t b = tl & 1u;
     const Place<kPair, E> w(p, sh, j, it, quad_, half, lane);
     float* diag = sh.diag[4 * half + quad_];
+    // other CTAs' results are read below: see them
+    bool ok = true;
+    if (j.mat != seen && (E != kGram || it > 0)) {
+      if (lane == 0) ok = wait_count(muon_counts(p.ws) + j.mat, units_before<kPair, E>(sh, j.mat, it), muon_status(p.ws), abort);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      seen = j.mat;
+    }
+    if ((kPair || E != kGram) && !ok) return false;
     Ahead a;
     look_ahead<kPair, E>(p, w, a, diag, it, lane);
-    const int got = lane == 0 ? (mbar_wait(&sh.acc_full[b], (tl >> 1) & 1u, muon_status(p.ws), abort) ? 1 : 0) : 0;
-    bool ok = __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
+    if (ok && lane == 0) ok = mbar_wait(&sh.acc_full[b], (tl >> 1) & 1u, muon_status(p.ws), abort);
+    ok = __all_sync(0xFFFFFFFFu, ok);
     if (!kPair && E == kGram) {
       // the warps meet in split units: all go on, or none
       if (!ok && lane == 0) *abort = 1;
@@ -629,8 +664,12 @@ __device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, uint32_t& 
     if (lane == 0) {
       if (rank == 0) mbar_arrive(&sh.acc_empty[b]);
       else mbar_arrive_remote(cluster_map(smem_addr(&sh.acc_empty[b]), 0));
+      // this warp's results (__syncwarp orders the lanes' before the release); a producer that
+      // sees the count fences its TMA copies behind it
+      asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(muon_counts(p.ws) + j.mat), "r"(1u) : "memory");
     }
   }
+  deal.skip(total);
   return true;
 }
 
@@ -660,7 +699,6 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
       mbar_init(&sh.acc_full[b], 1);
       mbar_init(&sh.acc_empty[b], kPair ? 16 : 8);
     }
-    mbar_init(&sh.go, 1);
     mbar_init(&sh.done, 1);
     sh.abort = 0;
     fence_mbar_init();
@@ -681,23 +719,17 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
   }
   tc_fence_after();
   const uint32_t tmem = sh.tmem, base = smem_addr(smem);
-  const uint32_t* count = muon_barrier(p.ws);
 
   if (warp == 0) {
     if (lane == 0) {
       Ring<kPair> ring;
+      Deal<kPair> deal;
       bool ok = true;
       for (int ph = 0; ph < 3 * p.K && ok; ++ph) {
-        if (ph > 0) {
-          ok = wait_count(count, (uint32_t)ph * gridDim.x, status, abort);
-          mbar_arrive(&sh.go);
-          if (!ok) break;
-          fence_async();
-        }
         const int it = ph / 3, e = ph - 3 * it;
-        ok = e == kGram ? produce<kPair, kGram>(p, maps, sh, ring, it, base, rank, abort)
-             : e == kSquare ? produce<kPair, kSquare>(p, maps, sh, ring, it, base, rank, abort)
-                            : produce<kPair, kUpdate>(p, maps, sh, ring, it, base, rank, abort);
+        ok = e == kGram ? produce<kPair, kGram>(p, maps, sh, ring, deal, it, base, rank, abort)
+             : e == kSquare ? produce<kPair, kSquare>(p, maps, sh, ring, deal, it, base, rank, abort)
+                            : produce<kPair, kUpdate>(p, maps, sh, ring, deal, it, base, rank, abort);
       }
       // every copy lands before the pair may exit (they count on the leader's barriers)
       if (rank == 0) {
@@ -710,13 +742,14 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       Ring<kPair> ring;
+      Deal<kPair> deal;
       uint32_t tl = 0;
       bool ok = true;
       for (int ph = 0; ph < 3 * p.K && ok; ++ph) {
         const int e = ph % 3;
-        ok = e == kGram ? multiply<kPair, kGram>(p, sh, ring, tl, base, tmem, abort)
-             : e == kSquare ? multiply<kPair, kSquare>(p, sh, ring, tl, base, tmem, abort)
-                            : multiply<kPair, kUpdate>(p, sh, ring, tl, base, tmem, abort);
+        ok = e == kGram ? multiply<kPair, kGram>(p, sh, ring, deal, tl, base, tmem, abort)
+             : e == kSquare ? multiply<kPair, kSquare>(p, sh, ring, deal, tl, base, tmem, abort)
+                            : multiply<kPair, kUpdate>(p, sh, ring, deal, tl, base, tmem, abort);
       }
       if constexpr (kPair) tc_commit_pair(&sh.done);
       else tc_commit(&sh.done);
@@ -725,25 +758,14 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
     }
   } else {
     const int quad_ = warp & 3, half = (warp - 2) >> 2;
+    Deal<kPair> deal;
     uint32_t tl = 0;
     bool ok = true;
-    for (int ph = 0; ph < 3 * p.K; ++ph) {
+    for (int ph = 0; ph < 3 * p.K && ok; ++ph) {
       const int it = ph / 3, e = ph - 3 * it;
-      if (ph > 0 && ok) {                 // other CTAs' results are read below
-        const int got = lane == 0 ? (mbar_wait(&sh.go, (uint32_t)(ph - 1) & 1u, status, abort) ? 1 : 0) : 0;
-        ok = __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
-        __syncwarp();
-      }
-      if (ok)
-        ok = e == kGram ? finish<kPair, kGram>(p, sh, tl, it, tmem, rank, quad_, half, lane, abort)
-             : e == kSquare ? finish<kPair, kSquare>(p, sh, tl, it, tmem, rank, quad_, half, lane, abort)
-                            : finish<kPair, kUpdate>(p, sh, tl, it, tmem, rank, quad_, half, lane, abort);
-      // every thread's results before the count (the barrier orders them before the release);
-      // a producer that sees the count fences its TMA copies behind it
-      named_bar(1, 256);
-      if (threadIdx.x == 64) {
-        asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(muon_barrier(p.ws)), "r"(1u) : "memory");
-      }
+      ok = e == kGram ? finish<kPair, kGram>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort)
+           : e == kSquare ? finish<kPair, kSquare>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort)
+                          : finish<kPair, kUpdate>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort);
     }
   }
   __syncwarp();
