@@ -13,12 +13,13 @@
 // integer, so f' <= fraction 2^22 decides the same with the fraction cut to its integer part.
 // A block that holds NaN or Inf: scale byte 255 (NaN), codes 0.
 //
-// One pass: each CTA reads a 128 x 128 tile once (eight elements a thread and step, four
-// threads a 32-element block) and writes the row view from registers; the column view
+// One pass: each CTA reads a 128 x 128 tile once (four pieces of sixteen elements a thread, all
+// loads first, two threads a 32-element block) and writes the row view from registers; the column view
 // reads the tile back from shared memory, one thread a column (FP32) or a pair of columns
 // (16-bit types), and both views' scales leave as whole 512-byte atoms.  Bound by HBM: in
 // bytes per element the input's size plus 17/32 for each view.
 #include <cstdint>
+#include <type_traits>
 
 #include "mx_device.cuh"
 #include "mx_internal.h"
@@ -33,7 +34,6 @@ constexpr uint64_t kMxColumnSeed = 0xD1B54A32D192ED03ull;
 template <typename T> struct MxIo;
 template <> struct MxIo<float> {
   static constexpr int kVec = 2;                        // 16-byte loads for 8 elements
-  static __device__ __forceinline__ float get(const float* p) { return __ldg(p); }
   static __device__ __forceinline__ void unpack(const uint4* w, float* x) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
 #pragma unroll
@@ -47,7 +47,6 @@ template <> struct MxIo<float> {
 };
 template <> struct MxIo<__nv_bfloat16> {
   static constexpr int kVec = 1;
-  static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
   static __device__ __forceinline__ float lo(uint32_t u) { return __uint_as_float(u << 16); }
   static __device__ __forceinline__ float hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
   static __device__ __forceinline__ uint32_t two(float a, float b) { return pack_bf16x2(a, b); }
@@ -63,7 +62,6 @@ template <> struct MxIo<__nv_bfloat16> {
 };
 template <> struct MxIo<__half> {
   static constexpr int kVec = 1;
-  static __device__ __forceinline__ float get(const __half* p) { return __half2float(__ldg(p)); }
   static __device__ __forceinline__ float lo(uint32_t u) { return half_lo(u); }
   static __device__ __forceinline__ float hi(uint32_t u) { return half_hi(u); }
   static __device__ __forceinline__ uint32_t two(float a, float b) {
@@ -81,7 +79,36 @@ template <> struct MxIo<__half> {
   static __device__ __forceinline__ __half cast(float v) { return __float2half_rn(v); }
 };
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// Sixteen consecutive elements of T as they are in memory.
+template <typename T>
+struct Piece {
+  static constexpr int kWords = 4 * (int)sizeof(T);       // 32-bit words
+  uint32_t w[kWords];
+};
+
+// Largest |x| of the pieces' words, as a running maximum over packed magnitudes ...
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t m, uint32_t w) {
+  if constexpr (sizeof(T) == 4) return max(m, w & 0x7FFFFFFFu);
+  else return max_u16x2(m, w & 0x7FFF7FFFu);
+}
+// ... and float bits of a 16-bit magnitude (Inf and NaN stay Inf or NaN).
+template <typename T>
+__device__ __forceinline__ uint32_t magnitude_bits(uint32_t m16) {
+  if constexpr (std::is_same<T, __half>::value) return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m16)));
+  else return m16 << 16;
+}
+// Element i of packed words.
+template <typename T>
+__device__ __forceinline__ float element(const uint32_t* w, int i) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+  else return (i & 1) ? MxIo<T>::hi(w[i >> 1]) : MxIo<T>::lo(w[i >> 1]);
+}
 
 // Eight codes of x[0..7], nearest.
 __device__ __forceinline__ uint32_t mx_codes8(const float* x, float inv) {
@@ -90,25 +117,27 @@ __device__ __forceinline__ uint32_t mx_codes8(const float* x, float inv) {
 
 // One code, stochastic.  Adding 1 (towards zero) to v < 1 gives every interval of the grid
 // below 1 the form 1.m, so bit 22 upwards of the float counts grid points and the 22 bits
-// below are the fraction of the interval.
-__device__ __forceinline__ uint32_t mx_code_sr(float x, float inv, uint32_t f) {
+// below are the fraction F of the interval.  64 f + 32 <= F exactly when F + 64 (65535 - f) + 32
+// carries into bit 22; `nf` is 65535 - f.
+__device__ __forceinline__ uint32_t mx_code_sr(float x, float inv, uint32_t nf) {
   const float v = fminf(fabsf(x * inv), 6.0f);
   const bool small = v < 1.0f;
   const uint32_t b = __float_as_uint(small ? __fadd_rz(v, 1.0f) : v);
-  uint32_t code = (b >> 22) - (small ? 254u : 252u);
-  code += (64u * f + 32u <= (b & 0x3FFFFFu)) ? 1u : 0u;
-  return code | ((__float_as_uint(x) >> 31) << 3);
+  const uint32_t code = ((b + 64u * nf + 32u) >> 22) - (small ? 254u : 252u);
+  return code | ((__float_as_uint(x) >> 28) & 8u);
 }
 
-// Eight codes of view elements (r, c) .. (r, c + 7), stochastic; c % 8 == 0.
+// Eight codes of view elements (r, c) .. (r, c + 7), stochastic; group = the first's group of four.
 __device__ __forceinline__ uint32_t mx_codes8_sr(const float* x, float inv, uint64_t seed, int64_t group) {
   uint32_t w = 0u;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint64_t z = splitmix64(seed, (uint64_t)(group + h));
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w |= mx_code_sr(x[4 * h + j], inv, (uint32_t)(z >> (16 * j)) & 0xFFFFu) << (4 * (4 * h + j));
+  for (int h = 1; h >= 0; --h) {
+    const uint64_t z = ~splitmix64(seed, (uint64_t)(group + h));
+    const uint32_t lo = (uint32_t)z, hi = (uint32_t)(z >> 32);
+    w = 16u * w + mx_code_sr(x[4 * h + 3], inv, hi >> 16);
+    w = 16u * w + mx_code_sr(x[4 * h + 2], inv, hi & 0xFFFFu);
+    w = 16u * w + mx_code_sr(x[4 * h + 1], inv, lo >> 16);
+    w = 16u * w + mx_code_sr(x[4 * h], inv, lo & 0xFFFFu);
   }
   return w;
 }
@@ -123,15 +152,15 @@ struct MxQuantArgs {
   uint64_t seed;
   int32_t tiled;
   int32_t ceil_rule;
-  int32_t vec;        // rows start on 16-byte boundaries
+  int32_t vec;        // rows start on 32-byte (2) or 16-byte (1) boundaries
 };
 
-// `bytes` (4 or 16) code bytes of row r of a PLAIN view at byte b0, cut at the row's end.
+// `kBytes` (8 or 16) code bytes of row r of a PLAIN view at byte b0, cut at the row's end.
 template <int kBytes>
 __device__ __forceinline__ void plain_store(uint8_t* codes, int64_t r, int64_t b0, int64_t row_bytes, const uint32_t* w) {
   uint8_t* p = codes + r * row_bytes + b0;
   if (b0 + kBytes <= row_bytes && (reinterpret_cast<uintptr_t>(p) & (kBytes - 1)) == 0) {
-    if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
+    if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     return;
   }
@@ -155,58 +184,83 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_quantize_kernel(const __grid
   const int64_t row_cp = (a.cols + 255) & ~int64_t(255), col_cp = (a.rows + 255) & ~int64_t(255);
   // the row view's padding ends at rows % 128, the column view's at cols % 128
   const bool row_in = kRow && (a.tiled ? r0 < ((a.rows + 127) & ~int64_t(127)) && c0 < row_cp : true);
-  const int rr = lane >> 4, ch = lane & 15;    // two rows a warp and step, eight columns a lane
-  const int64_t c = c0 + 8 * ch;
+  // four rows a warp and step, sixteen columns a lane, two lanes a block
+  const int rr = lane >> 3, ch = lane & 7;
+  const int64_t c = c0 + 16 * ch;
   const int64_t groups = (a.cols + 3) >> 2;
-#pragma unroll 1
-  for (int s0 = 0; s0 < 8; s0 += 4) {
-    if (!a.tiled && r0 + 16 * s0 >= a.rows && !kCol) break;
-    float xv[4][8];
+  uint8_t* const row_tile = a.row_codes + ((r0 >> 7) * (row_cp >> 8) + (c0 >> 8)) * kTileBytes + 8 * (lane & 1);
+  const int row_chunk = (int)((c0 & 255) >> 5) + (ch >> 1);
+  constexpr int kSteps = 4;
+  Piece<T> piece[kSteps];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int64_t r = r0 + 16 * (s0 + s) + 2 * warp + rr;
-      const T* p = x + r * a.ld + c;
-      if (r < a.rows && c + 8 <= a.cols && a.vec) {
-        uint4 w[MxIo<T>::kVec];
+  for (int s = 0; s < kSteps; ++s) {
+    const int64_t r = r0 + 32 * s + 4 * warp + rr;
+    const T* p = x + r * a.ld + c;
+    uint32_t* w = piece[s].w;
+    if (r < a.rows && c + 16 <= a.cols && a.vec) {
+      if (a.vec == 2) {
 #pragma unroll
-        for (int q = 0; q < MxIo<T>::kVec; ++q) w[q] = __ldg(reinterpret_cast<const uint4*>(p) + q);
-        MxIo<T>::unpack(w, xv[s]);
+        for (int q = 0; q < Piece<T>::kWords / 8; ++q)
+          asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                       : "=r"(w[8 * q]), "=r"(w[8 * q + 1]), "=r"(w[8 * q + 2]), "=r"(w[8 * q + 3]), "=r"(w[8 * q + 4]),
+                         "=r"(w[8 * q + 5]), "=r"(w[8 * q + 6]), "=r"(w[8 * q + 7])
+                       : "l"(reinterpret_cast<const uint8_t*>(p) + 32 * q));
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xv[s][i] = (r < a.rows && c + i < a.cols) ? MxIo<T>::get(p + i) : 0.0f;
+        for (int q = 0; q < Piece<T>::kWords / 4; ++q) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + q);
+          w[4 * q] = u.x; w[4 * q + 1] = u.y; w[4 * q + 2] = u.z; w[4 * q + 3] = u.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < Piece<T>::kWords; ++i) w[i] = 0u;
+      if (r < a.rows) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (c + i >= a.cols) continue;
+          if constexpr (sizeof(T) == 4) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+          else w[i >> 1] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + i) << (16 * (i & 1));
+        }
       }
     }
+  }
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int tr = 16 * (s0 + s) + 2 * warp + rr;
-      const int64_t r = r0 + tr;
-      if constexpr (kCol) {
-        uint4 w[MxIo<T>::kVec];
-        MxIo<T>::pack(xv[s], w);                // exact: the values came from T
+  for (int s = 0; s < kSteps; ++s) {
+    const int tr = 32 * s + 4 * warp + rr;
+    const int64_t r = r0 + tr;
+    const uint32_t* w = piece[s].w;
+    if constexpr (kCol) {
 #pragma unroll
-        for (int q = 0; q < MxIo<T>::kVec; ++q) reinterpret_cast<uint4*>(tile + tr * kMxTile + 8 * ch)[q] = w[q];
+      for (int q = 0; q < Piece<T>::kWords / 4; ++q)
+        reinterpret_cast<uint4*>(tile + tr * kMxTile + 16 * ch)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    }
+    if constexpr (kRow) {
+      if (!a.tiled && r0 + 32 * s >= a.rows) continue;       // (uniform)
+      uint32_t m = 0u;
+#pragma unroll
+      for (int i = 0; i < Piece<T>::kWords; ++i) m = max_magnitude<T>(m, w[i]);
+      if constexpr (sizeof(T) == 2) m = magnitude_bits<T>(max(m & 0xFFFFu, m >> 16));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      const uint32_t byte = mx_scale_byte(m, ceil_rule);
+      uint32_t q[2] = {0u, 0u};
+      if (byte != 255u) {
+        const float inv = mx_inverse_scale(byte);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = element<T>(w, 8 * g + i);
+          q[g] = kSr ? mx_codes8_sr(v, inv, a.seed, r * groups + (c >> 2) + 2 * g) : mx_codes8(v, inv);
+        }
       }
-      if constexpr (kRow) {
-        uint32_t m = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(xv[s][i]));
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const uint32_t byte = mx_scale_byte(m, ceil_rule);
-        uint32_t w = 0u;
-        if (byte != 255u) {
-          const float inv = mx_inverse_scale(byte);
-          w = kSr ? mx_codes8_sr(xv[s], inv, a.seed, r * groups + (c >> 2)) : mx_codes8(xv[s], inv);
-        }
-        if (a.tiled) {
-          if (row_in)
-            *reinterpret_cast<uint32_t*>(a.row_codes + tiled_chunk_offset(r, c & ~int64_t(31), row_cp) + ((c & 31) >> 1)) = w;
-          if ((lane & 3) == 0) row_atom[16 * (tr & 31) + 4 * (tr >> 5) + (ch >> 2)] = (uint8_t)byte;
-        } else if (r < a.rows && c < a.cols) {
-          // an odd row's last nibble is 0: its element was read as 0
-          plain_store<4>(a.row_codes, r, c >> 1, (a.cols + 1) >> 1, &w);
-          if ((lane & 3) == 0) a.row_scales[r * ((a.cols + 31) >> 5) + (c >> 5)] = (uint8_t)byte;
-        }
+      if (a.tiled) {
+        if (row_in) *reinterpret_cast<uint2*>(row_tile + 128 * tr + ((row_chunk ^ (tr & 7)) << 4)) = make_uint2(q[0], q[1]);
+        if ((lane & 1) == 0) row_atom[16 * (tr & 31) + 4 * (tr >> 5) + (ch >> 1)] = (uint8_t)byte;
+      } else if (r < a.rows && c < a.cols) {
+        // an odd row's last nibble is 0: its element was read as 0
+        plain_store<8>(a.row_codes, r, c >> 1, (a.cols + 1) >> 1, q);
+        if ((lane & 1) == 0) a.row_scales[r * ((a.cols + 31) >> 5) + (c >> 5)] = (uint8_t)byte;
       }
     }
   }
@@ -219,22 +273,20 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_quantize_kernel(const __grid
     const uint32_t* words = reinterpret_cast<const uint32_t*>(tile);
     const int64_t cgroups = (a.rows + 3) >> 2;
     const uint64_t cseed = a.seed ^ kMxColumnSeed;
+    uint8_t* const col_tile = a.col_codes + ((c0 >> 7) * (col_cp >> 8) + (r0 >> 8)) * kTileBytes;
+    const int col_chunk = (int)((r0 & 255) >> 5);
 #pragma unroll
     for (int t = 0; t < kTasks; ++t) {
       const int task = threadIdx.x + t * kMxThreads;
       const int cw = task % (kMxTile / kPair), blk = task / (kMxTile / kPair);
-      uint32_t w[32];
+      uint32_t w[32], m2 = 0u;
 #pragma unroll
       for (int i = 0; i < 32; ++i) w[i] = words[(32 * blk + i) * (kMxTile / kPair) + cw];
 #pragma unroll
-      for (int h = 0; h < kPair; ++h) {
-        auto value = [&](int i) -> float {
-          if constexpr (kPair == 1) return __uint_as_float(w[i]);
-          else return h ? MxIo<T>::hi(w[i]) : MxIo<T>::lo(w[i]);
-        };
-        uint32_t m = 0u;
+      for (int i = 0; i < 32; ++i) m2 = max_magnitude<T>(m2, w[i]);      // both columns of a word
 #pragma unroll
-        for (int i = 0; i < 32; ++i) m = max(m, abs_bits(value(i)));
+      for (int h = 0; h < kPair; ++h) {
+        const uint32_t m = kPair == 1 ? m2 : magnitude_bits<T>(h ? m2 >> 16 : m2 & 0xFFFFu);
         const uint32_t byte = mx_scale_byte(m, ceil_rule);
         uint32_t q[4] = {0u, 0u, 0u, 0u};
         const int tc = kPair * cw + h;
@@ -245,13 +297,16 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_quantize_kernel(const __grid
           for (int g = 0; g < 4; ++g) {
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = value(8 * g + i);
+            for (int i = 0; i < 8; ++i) {
+              if constexpr (kPair == 1) v[i] = __uint_as_float(w[8 * g + i]);
+              else v[i] = h ? MxIo<T>::hi(w[8 * g + i]) : MxIo<T>::lo(w[8 * g + i]);
+            }
             q[g] = kSr ? mx_codes8_sr(v, inv, cseed, vr * cgroups + ((vc + 8 * g) >> 2)) : mx_codes8(v, inv);
           }
         }
         if (a.tiled) {
           if (col_in)
-            *reinterpret_cast<uint4*>(a.col_codes + tiled_chunk_offset(vr, vc, col_cp)) = make_uint4(q[0], q[1], q[2], q[3]);
+            *reinterpret_cast<uint4*>(col_tile + 128 * tc + (((col_chunk + blk) ^ (tc & 7)) << 4)) = make_uint4(q[0], q[1], q[2], q[3]);
           col_atom[16 * (tc & 31) + 4 * (tc >> 5) + blk] = (uint8_t)byte;
         } else if (vr < a.cols && vc < a.rows) {
           plain_store<16>(a.col_codes, vr, vc >> 1, (a.rows + 1) >> 1, q);
@@ -393,7 +448,8 @@ cudaError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_
                                   bool stochastic, uint64_t seed, cudaStream_t st) {
   MxQuantArgs a{x, rows, cols, ld, row_codes, row_scales, col_codes, col_scales, seed, tiled, ceil_rule, 0};
   const int64_t size = dtype == kTypeF32 ? 4 : 2;
-  a.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (rows == 1 || ld * size % 16 == 0);
+  const auto starts_on = [&](uintptr_t n) { return reinterpret_cast<uintptr_t>(x) % n == 0 && (rows == 1 || (uintptr_t)(ld * size) % n == 0); };
+  a.vec = starts_on(32) ? 2 : starts_on(16) ? 1 : 0;
   switch (dtype) {
     case kTypeF32: return launch_quant_type<float>(a, stochastic, st);
     case kTypeBf16: return launch_quant_type<__nv_bfloat16>(a, stochastic, st);
