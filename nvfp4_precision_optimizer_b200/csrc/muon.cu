@@ -108,47 +108,55 @@ __global__ void __launch_bounds__(kThreads, 2) muon_moment_kernel(const __grid_c
       }
     }
   } else {
+    const bool flat = d.ldg == gcols && (!d.mom || d.ldm == gcols);
     const int32_t count = (r1 - r0) * gcols;
-    for (int32_t i = threadIdx.x; i < count; i += kThreads) {
-      const int64_t r = r0 + i / gcols, c = i % gcols;
-      float g = get1(d.g, r * d.ldg + c, d.tg);
-      if (d.mom) {
-        const float m = put1(d.mom, r * d.ldm + c, d.tm, fmaf(p.beta, get1(d.mom, r * d.ldm + c, d.tm), p.rest * g));
-        g = direction(p, m, g);
+    for (int32_t i0 = threadIdx.x; i0 < count; i0 += 8 * kThreads) {
+      int64_t ag[8], am[8];
+      float g[8], m[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int32_t i = i0 + k * kThreads;
+        const int64_t r = flat ? r0 : r0 + i / gcols, c = flat ? i : i % gcols;
+        ag[k] = i < count ? r * d.ldg + c : -1;
+        am[k] = i < count ? r * d.ldm + c : -1;
       }
-      sum += (double)g * (double)g;
+      gather8(d.g, d.tg, ag, g);
+      if (d.mom) {
+        gather8(d.mom, d.tm, am, m);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (am[k] < 0) continue;
+          m[k] = put1(d.mom, am[k], d.tm, fmaf(p.beta, m[k], p.rest * g[k]));
+          g[k] = direction(p, m[k], g[k]);
+        }
+      }
+      sum += squares8(g);
     }
   }
   const double s = block_sum(sum, red);
   if (threadIdx.x == 0) muon_partials(p.ws)[d.partial + part] = s;
 }
 
-// Eight elements of U from (r, c) of G on: in memory's form, then their values; absent ones are 0.
-struct RawU {
-  Raw8 g, m;
+// Eight elements of U that may be absent or off a 16-byte boundary: out of line, so that its
+// registers do not crowd the aligned case.
+struct Eight {
+  float v[8];
 };
-__device__ __forceinline__ bool whole8(bool vec, int64_t r, int64_t c, int64_t rows, int64_t cols) {
-  return vec && r < rows && c + 8 <= cols;
-}
-__device__ __forceinline__ void load_direction8(const MuonMat& d, bool whole, int64_t r, int64_t c, RawU& x) {
-  if (!whole) return;
-  x.g = load8(d.g, r * d.ldg + c, d.tg);
-  if (d.mom) x.m = load8(d.mom, r * d.ldm + c, d.tm);
-}
-__device__ __forceinline__ void direction8(const MuonCall& p, const MuonMat& d, bool whole, int64_t r, int64_t c, int64_t rows,
-                                           int64_t cols, const RawU& raw, float* x) {
-  if (whole) {
-    unpack8(raw.g, d.tg, x);
-    if (d.mom) {
-      float m[8];
-      unpack8(raw.m, d.tm, m);
+__device__ __noinline__ Eight guarded_direction8(const MuonCall& p, const MuonMat& d, int64_t r, int64_t c, int64_t rows, int64_t cols) {
+  Eight x;
+  int64_t at[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = direction(p, m[k], x[k]);
-    }
-  } else {
+  for (int k = 0; k < 8; ++k) at[k] = (r < rows && c + k < cols) ? r * d.ldg + c + k : -1;
+  gather8(d.g, d.tg, at, x.v);
+  if (d.mom) {
+    float m[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = (r < rows && c + k < cols) ? direction_at(p, d, r, c + k) : 0.0f;
+    for (int k = 0; k < 8; ++k) at[k] = (r < rows && c + k < cols) ? r * d.ldm + c + k : -1;
+    gather8(d.mom, d.tm, at, m);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x.v[k] = direction(p, m[k], x.v[k]);
   }
+  return x;
 }
 
 // Persistent, a contiguous range of 128 x 64 tiles of X_0 a CTA.  A tall matrix's tile turns in
@@ -193,17 +201,32 @@ __global__ void __launch_bounds__(kThreads, 2) muon_prepare_kernel(const __grid_
     auto row_of = [&](int q) -> int64_t { return d.tall ? c0 + (q >> 4) : r0 + (q >> 3); };
     auto col_of = [&](int q) -> int64_t { return d.tall ? r0 + 8 * (q & 15) : c0 + 8 * (q & 7); };
     float x[kAhead][8];
-    {
-      RawU raw[kAhead];
+    // tiles inside the matrix, on 16-byte boundaries: all loads first
+    if (vec && r0 + 128 <= d.m && c0 + 64 <= d.n) {
+      Raw8 g[kAhead], m[kAhead];
 #pragma unroll
       for (int s = 0; s < kAhead; ++s) {
         const int q = threadIdx.x + s * kThreads;
-        load_direction8(d, whole8(vec, row_of(q), col_of(q), grows, gcols), row_of(q), col_of(q), raw[s]);
+        g[s] = load8(d.g, row_of(q) * d.ldg + col_of(q), d.tg);
+        if (d.mom) m[s] = load8(d.mom, row_of(q) * d.ldm + col_of(q), d.tm);
       }
 #pragma unroll
       for (int s = 0; s < kAhead; ++s) {
+        unpack8(g[s], d.tg, x[s]);
+        if (d.mom) {
+          float v[8];
+          unpack8(m[s], d.tm, v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[s][k] = direction(p, v[k], x[s][k]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
         const int q = threadIdx.x + s * kThreads;
-        direction8(p, d, whole8(vec, row_of(q), col_of(q), grows, gcols), row_of(q), col_of(q), grows, gcols, raw[s], x[s]);
+        const Eight e = guarded_direction8(p, d, row_of(q), col_of(q), grows, gcols);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[s][k] = e.v[k];
       }
     }
     if (d.tall) {

@@ -18,14 +18,14 @@ __device__ __forceinline__ int owner_of(const int32_t* prefix, int count, int32_
   return lo;
 }
 
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float get1(const void* p, int64_t i, int type) {
   if (type == kTypeF32) return static_cast<const float*>(p)[i];
   if (type == kTypeBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
   return __half2float(static_cast<const __half*>(p)[i]);
 }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 // Round to the type and back: what a later read sees.
 __device__ __forceinline__ float put1(void* p, int64_t i, int type, float v) {
   if (type == kTypeF32) {
@@ -82,6 +82,23 @@ __device__ __forceinline__ void unpack8(const Raw8& r, int type, float* v) {
     }
   }
 }
+// Eight elements at[i], absent where it is negative (0): the loads are in flight together.
+template <typename T>
+__device__ __forceinline__ void gather8_as(const void* p, const int64_t* at, float* v) {
+  const T* q = static_cast<const T*>(p);
+  T raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (at[i] >= 0) raw[i] = q[at[i]];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = at[i] >= 0 ? to_f32(raw[i]) : 0.0f;
+}
+__device__ __forceinline__ void gather8(const void* p, int type, const int64_t* at, float* v) {
+  if (type == kTypeF32) gather8_as<float>(p, at, v);
+  else if (type == kTypeBf16) gather8_as<__nv_bfloat16>(p, at, v);
+  else gather8_as<__half>(p, at, v);
+}
+
 // Store and replace by what was stored.
 __device__ __forceinline__ void put8(void* p, int64_t i, int type, float* v) {
   if (type == kTypeF32) {
@@ -109,12 +126,6 @@ __device__ __forceinline__ void put8(void* p, int64_t i, int type, float* v) {
 
 __device__ __forceinline__ float direction(const MuonCall& p, float mom, float g) {
   return p.nesterov ? fmaf(p.beta, mom, p.rest * g) : mom;
-}
-
-// Update direction at (r, c) of G.
-__device__ __forceinline__ float direction_at(const MuonCall& p, const MuonMat& d, int64_t r, int64_t c) {
-  const float g = get1(d.g, r * d.ldg + c, d.tg);
-  return d.mom ? direction(p, get1(d.mom, r * d.ldm + c, d.tm), g) : g;
 }
 
 // FP16 parts of eight values: value = high + low, to 22 significand bits or 2^-25, whichever is

@@ -244,8 +244,10 @@ __device__ __forceinline__ Pair ordered(const Pair& r, bool swap) {
 __device__ __forceinline__ uint4 quad(const Pair& p, int i) { return make_uint4(p.w[4 * i], p.w[4 * i + 1], p.w[4 * i + 2], p.w[4 * i + 3]); }
 
 // 32 results (columns col .. col + 31 of working row `row`) into the weights or the output.
+// Returns whether a result is not finite.
 template <typename T>
-__device__ __forceinline__ void write_result(const MuonCall& p, const MuonMat& d, int32_t row, int32_t col, float* y, int lane, bool& bad) {
+__device__ __forceinline__ bool write_result(const MuonCall& p, const MuonMat& d, int32_t row, int32_t col, float* y, int lane) {
+  bool bad = false;
   constexpr int kPer = 32 / (int)sizeof(T);                  // elements of 32 bytes
   const bool blend = p.rate >= 0.0f;
   auto result = [&](float x, float w) -> float {
@@ -254,53 +256,46 @@ __device__ __forceinline__ void write_result(const MuonCall& p, const MuonMat& d
     return blend ? fmaf(-p.rate, u, p.keep * w) : u;
   };
   T* w = static_cast<T*>(d.w);
+  // in each case the old weights' loads are in flight together
   if (!d.tall && col + 32 <= d.n && ((reinterpret_cast<uintptr_t>(w) | (uintptr_t)(d.ldw * (int64_t)sizeof(T))) & 31) == 0) {
-    if (row >= d.m) return;
+    if (row >= d.m) return false;
     T* at = w + row * d.ldw + col;
 #pragma unroll
-    for (int q = 0; q < 32 / kPer; ++q) {
-      Pair r{};
-      if (blend) r = load_pair(at + q * kPer);
-      T* e = reinterpret_cast<T*>(r.w);
+    for (int q = 0; q < 32 / kPer; q += 2) {
+      Pair r[2]{};
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if constexpr (sizeof(T) == 4) e[i] = result(y[q * kPer + i], e[i]);
-        else if constexpr (std::is_same<T, __half>::value) e[i] = __float2half_rn(result(y[q * kPer + i], __half2float(e[i])));
-        else e[i] = __float2bfloat16_rn(result(y[q * kPer + i], __bfloat162float(e[i])));
+      for (int b = 0; b < 2; ++b)
+        if (blend) r[b] = load_pair(at + (q + b) * kPer);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        T* e = reinterpret_cast<T*>(r[b].w);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+        put_as(e + i, result(y[(q + b) * kPer + i], blend ? get_as(e + i) : 0.0f));
+        }
+        store_pair(at + (q + b) * kPer, r[b]);
       }
-      store_pair(at + q * kPer, r);
     }
-    return;
+    return bad;
   }
-  if (d.tall) {               // neighbouring lanes hold neighbouring elements
+  // Neighbouring lanes hold neighbouring elements of a tall matrix's rows.  Rows that do not start
+  // on 32 bytes: the warp's 32 x 32 values change places first.
+  uint32_t* v = reinterpret_cast<uint32_t*>(y);
+  if (!d.tall) turn32(v, lane);
+  const int32_t r0 = d.tall ? row : row - lane, c0 = d.tall ? col : col + lane;      // of value 0
+  if (r0 >= d.m || c0 >= d.n) return false;
+  const int32_t count = min(32, d.tall ? d.n - c0 : d.m - r0);
+  T* at = w + (d.tall ? (int64_t)c0 * d.ldw + r0 : (int64_t)r0 * d.ldw + c0);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (col + i >= d.n || row >= d.m) break;
-      T* at = w + (int64_t)(col + i) * d.ldw + row;
-      put_as(at, result(y[i], blend ? get_as(at) : 0.0f));
-    }
-    return;
+  for (int h = 0; h < 32; h += 8) {
+    float old[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) old[i] = (blend && h + i < count) ? get_as(at + (h + i) * d.ldw) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (h + i < count) put_as(at + (h + i) * d.ldw, result(y[h + i], old[i]));
   }
-  // rows that do not start on 32 bytes: the warp's 32 x 32 values change places (lane and
-  // register), then a row at a time
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (i & s) continue;
-      const float got = __shfl_xor_sync(0xFFFFFFFFu, (lane & s) ? y[i] : y[i + s], s);
-      if (lane & s) y[i] = got;
-      else y[i + s] = got;
-    }
-  }
-  const int32_t r0 = row - lane;
-  if (col + lane >= d.n) return;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    if (r0 + i >= d.m) break;
-    T* at = w + (int64_t)(r0 + i) * d.ldw + col + lane;
-    put_as(at, result(y[i], blend ? get_as(at) : 0.0f));
-  }
+  return bad;
 }
 
 // Input of 32 columns: A or X, high and low parts.
@@ -360,11 +355,11 @@ struct Ahead {
   Input in[2];
   float own;             // d_i (Square) or a + e_i (Update)
 };
-template <bool kPair, int E>
+template <bool kPair, int E, bool kLast>
 __device__ __forceinline__ void look_ahead(const MuonCall& p, const Place<kPair, E>& w, Ahead& a, float* diag, int it, int lane) {
   if constexpr (E == kGram) return;
   w.load(a.in[0], 0);
-  if constexpr (kPair) w.load(a.in[1], 32);
+  if constexpr (kPair && !kLast) w.load(a.in[1], 32);
   if constexpr (E == kSquare) {
     a.own = __ldcg(w.da + w.row);
     __syncwarp();
@@ -376,10 +371,11 @@ __device__ __forceinline__ void look_ahead(const MuonCall& p, const Place<kPair,
   }
 }
 
-template <bool kPair, int E>
+// kLast: the last update, which writes the weights or the output (an instance of its own, so that
+// its registers do not crowd the others).
+template <bool kPair, int E, bool kLast>
 __device__ __forceinline__ void epilogue(const MuonCall& p, const Place<kPair, E>& w, Ahead& a, const float* diag, const MuonMat* m, int it,
                                          uint32_t taddr, int lane, const float* summed) {
-  const bool last = E == kUpdate && it == p.K - 1;
   const float* poly = p.coeffs + (p.n_coeffs == 1 ? 0 : 3 * it);
   const float pb = poly[1], pc = poly[2];
   bool bad = false;
@@ -410,9 +406,11 @@ __device__ __forceinline__ void epilogue(const MuonCall& p, const Place<kPair, E
       }
     } else {
       const Input in = a.in[0];
-      if constexpr (kPair) {
+      if constexpr (kPair && !kLast) {
         a.in[0] = a.in[1];
         if (c < 64) w.load(a.in[1], c + 64);       // the input two steps on
+      } else if constexpr (kPair) {
+        if (c < 96) w.load(a.in[0], c + 32);       // (registers: one step on)
       }
       float e = 0.0f;
 #pragma unroll
@@ -444,12 +442,12 @@ __device__ __forceinline__ void epilogue(const MuonCall& p, const Place<kPair, E
           if (lane == i) v[i] = 0.0f;
       }
     }
-    if (last) {
+    if constexpr (kLast) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= 1.0f / kXScale;
-      if (m->tw == kTypeF32) write_result<float>(p, *m, w.row, col, v, lane, bad);
-      else if (m->tw == kTypeBf16) write_result<__nv_bfloat16>(p, *m, w.row, col, v, lane, bad);
-      else write_result<__half>(p, *m, w.row, col, v, lane, bad);
+      if (m->tw == kTypeF32) bad |= write_result<float>(p, *m, w.row, col, v, lane);
+      else if (m->tw == kTypeBf16) bad |= write_result<__nv_bfloat16>(p, *m, w.row, col, v, lane);
+      else bad |= write_result<__half>(p, *m, w.row, col, v, lane);
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -462,7 +460,7 @@ __device__ __forceinline__ void epilogue(const MuonCall& p, const Place<kPair, E
       }
     }
   }
-  if (bad) atomicOr(muon_status(p.ws), kStatusNonFinite);
+  if (kLast && bad) atomicOr(muon_status(p.ws), kStatusNonFinite);
 }
 
 // ------------------------------------------------------------------ counts in the workspace
@@ -618,7 +616,7 @@ __device__ __forceinline__ bool sum_parts(const MuonCall& p, Shared& sh, const J
   return true;
 }
 
-template <bool kPair, int E>
+template <bool kPair, int E, bool kLast>
 __device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, Deal<kPair>& deal, uint32_t& tl, int it, uint32_t tmem, uint32_t rank, int quad_,
                                        int half, int lane, volatile int* abort) {
   using T = Tile<kPair>;
@@ -638,7 +636,7 @@ __device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, Deal<kPair
     }
     if ((kPair || E != kGram) && !ok) return false;
     Ahead a;
-    look_ahead<kPair, E>(p, w, a, diag, it, lane);
+    look_ahead<kPair, E, kLast>(p, w, a, diag, it, lane);
     if (ok && lane == 0) ok = mbar_wait(&sh.acc_full[b], (tl >> 1) & 1u, muon_status(p.ws), abort);
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (!kPair && E == kGram) {
@@ -655,9 +653,9 @@ __device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, Deal<kPair
     const MuonMat* m = &muon_table(p.ws)->mat[j.mat];
     if (!kPair && E == kGram && j.parts > 1) {
       float v[32];
-      if (sum_parts(p, sh, j, u, taddr, quad_, half, lane, v)) epilogue<kPair, E>(p, w, a, diag, m, it, taddr, lane, v);
+      if (sum_parts(p, sh, j, u, taddr, quad_, half, lane, v)) epilogue<kPair, E, kLast>(p, w, a, diag, m, it, taddr, lane, v);
     } else {
-      epilogue<kPair, E>(p, w, a, diag, m, it, taddr, lane, nullptr);
+      epilogue<kPair, E, kLast>(p, w, a, diag, m, it, taddr, lane, nullptr);
     }
     tc_fence_before();
     __syncwarp();
@@ -763,9 +761,10 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
     bool ok = true;
     for (int ph = 0; ph < 3 * p.K && ok; ++ph) {
       const int it = ph / 3, e = ph - 3 * it;
-      ok = e == kGram ? finish<kPair, kGram>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort)
-           : e == kSquare ? finish<kPair, kSquare>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort)
-                          : finish<kPair, kUpdate>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort);
+      ok = e == kGram ? finish<kPair, kGram, false>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort)
+           : e == kSquare ? finish<kPair, kSquare, false>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort)
+           : it < p.K - 1 ? finish<kPair, kUpdate, false>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort)
+                          : finish<kPair, kUpdate, true>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort);
     }
   }
   __syncwarp();

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_quantize_kernel(const __grid
     const int64_t r = r0 + 32 * s + 4 * warp + rr;
     const T* p = x + r * a.ld + c;
     uint32_t* w = piece[s].w;
-    if (r < a.rows && c + 16 <= a.cols && a.vec) {
+    if (r < a.rows && c + 16 <= a.cols) {
       if (a.vec == 2) {
 #pragma unroll
         for (int q = 0; q < Piece<T>::kWords / 8; ++q)
@@ -205,12 +205,19 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_quantize_kernel(const __grid
                        : "=r"(w[8 * q]), "=r"(w[8 * q + 1]), "=r"(w[8 * q + 2]), "=r"(w[8 * q + 3]), "=r"(w[8 * q + 4]),
                          "=r"(w[8 * q + 5]), "=r"(w[8 * q + 6]), "=r"(w[8 * q + 7])
                        : "l"(reinterpret_cast<const uint8_t*>(p) + 32 * q));
-      } else {
+      } else if (a.vec == 1) {
 #pragma unroll
         for (int q = 0; q < Piece<T>::kWords / 4; ++q) {
           const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + q);
           w[4 * q] = u.x; w[4 * q + 1] = u.y; w[4 * q + 2] = u.z; w[4 * q + 3] = u.w;
         }
+      } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < Piece<T>::kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+      } else if constexpr (sizeof(T) == 2) {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = (uint32_t)__ldg(h + 2 * i) | (uint32_t)__ldg(h + 2 * i + 1) << 16;
       }
     } else {
 #pragma unroll
@@ -375,20 +382,20 @@ struct MxDequantArgs {
 // four rows a warp at once so that four loads are in flight.  Bound by HBM.
 template <typename T>
 __global__ void __launch_bounds__(kMxThreads) mxfp4_dequantize_kernel(const __grid_constant__ MxDequantArgs a) {
+  __shared__ __align__(16) float turn[kMxThreads / 32][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t cp = (a.cols + 255) & ~int64_t(255);
   const int64_t segs = cp >> 8, groups = (a.rows + 3) >> 2, total = segs * groups;
   const int64_t row_bytes = (a.cols + 1) >> 1, row_blocks = (a.cols + 31) >> 5;
   for (int64_t t = (int64_t)blockIdx.x * (kMxThreads / 32) + warp; t < total; t += (int64_t)gridDim.x * (kMxThreads / 32)) {
     const int64_t rg = 4 * (t / segs), c = (t % segs) * 256 + 8 * lane;
-    if (c >= a.cols) continue;
     uint32_t w[4], byte[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t r = rg + i;
       w[i] = 0u;
       byte[i] = 0u;
-      if (r >= a.rows) continue;
+      if (r >= a.rows || c >= a.cols) continue;
       if (a.tiled) {
         w[i] = __ldg(reinterpret_cast<const uint32_t*>(a.codes + tiled_chunk_offset(r, c & ~int64_t(31), cp) + ((c & 31) >> 1)));
         byte[i] = __ldg(a.scales + mx_scale_offset(r, c >> 5, cp));
@@ -418,16 +425,28 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_dequantize_kernel(const __gr
         v[2 * k] = half_lo(h[k]) * s;
         v[2 * k + 1] = half_hi(h[k]) * s;
       }
-      T* y = static_cast<T*>(a.y) + r * a.ld + c;
-      if (a.vec && c + 8 <= a.cols) {
-        uint4 o[MxIo<T>::kVec];
-        MxIo<T>::pack(v, o);
+      T* y = static_cast<T*>(a.y) + r * a.ld;
+      if (a.vec) {
+        if (c + 8 <= a.cols) {
+          uint4 o[MxIo<T>::kVec];
+          MxIo<T>::pack(v, o);
 #pragma unroll
-        for (int k = 0; k < MxIo<T>::kVec; ++k) reinterpret_cast<uint4*>(y)[k] = o[k];
+          for (int k = 0; k < MxIo<T>::kVec; ++k) reinterpret_cast<uint4*>(y + c)[k] = o[k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (c + k < a.cols) y[c + k] = MxIo<T>::cast(v[k]);
+        }
       } else {
+        // rows that do not start on 16 bytes: neighbouring lanes store neighbouring elements
+        __syncwarp();
+        reinterpret_cast<float4*>(turn[warp])[2 * lane] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(turn[warp])[2 * lane + 1] = make_float4(v[4], v[5], v[6], v[7]);
+        __syncwarp();
+        const int64_t c0 = c - 8 * lane;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (c + k < a.cols) y[k] = MxIo<T>::cast(v[k]);
+          if (c0 + 32 * k + lane < a.cols) y[c0 + 32 * k + lane] = MxIo<T>::cast(turn[warp][32 * k + lane]);
       }
     }
   }

@@ -136,6 +136,20 @@ __device__ __forceinline__ void store_pair(void* p, const Pair& r) {
                : "memory");
 }
 
+// Transpose a warp's 32 x 32 words: v[i] of lane l becomes v[l] of lane i.
+__device__ __forceinline__ void turn32(uint32_t* v, int lane) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i & s) continue;
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, (lane & s) ? v[i] : v[i + s], s);
+      if (lane & s) v[i] = got;
+      else v[i + s] = got;
+    }
+  }
+}
+
 __device__ __forceinline__ float get_as(const float* p) { return *p; }
 __device__ __forceinline__ float get_as(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float get_as(const __half* p) { return __half2float(*p); }
