@@ -39,10 +39,13 @@ struct Plan {
 };
 
 // The plan depends on the sizes only.  Small calls are those whose products fit kMuonSmallUnits
-// tiles of the small kind.
+// tiles of the small kind and whose updates take at most kMuonSmallSteps K steps in all.  Both sides
+// (us for K = 5, small tiles and pairs): 256 x 8192 183 and 320, 1024 x 1024 160 and 196, 512 x 4096
+// (2048 steps) 221 and 244, 768 x 3000 (3384) 243 and 249, 1024 x 2048 (4096) 239 and 225, 1536 x
+// 1536 (6912) 305 and 240.
 Plan plan(int32_t count, const int64_t* rows, const int64_t* cols, MuonTable* t) {
   Plan pl;
-  int64_t parts = 0, updates = 0, grams = 0;
+  int64_t parts = 0, updates = 0, grams = 0, steps = 0;
   auto sides = [&](int32_t i, int32_t& m, int32_t& n) {
     m = (int32_t)(rows[i] < cols[i] ? rows[i] : cols[i]);
     n = (int32_t)(rows[i] < cols[i] ? cols[i] : rows[i]);
@@ -57,9 +60,10 @@ Plan plan(int32_t count, const int64_t* rows, const int64_t* cols, MuonTable* t)
     sides(i, m, n);
     if (m <= kMuonThin) continue;
     updates += (int64_t)muon_row_tiles(m) * muon_steps(n);
+    steps += (int64_t)muon_row_tiles(m) * muon_steps(n) * muon_steps(m);
     grams += muon_gram_tiles(m);
   }
-  pl.small = updates > 0 && updates <= kMuonSmallUnits && grams <= kMuonSmallUnits;
+  pl.small = updates > 0 && updates <= kMuonSmallUnits && grams <= kMuonSmallUnits && steps <= kMuonSmallSteps;
   int64_t off = up(kMuonPartials + 8 * parts, 1024);
   if (pl.small) {
     // the shortest parts, of 8 steps at least, that keep the Gram products' units in bounds

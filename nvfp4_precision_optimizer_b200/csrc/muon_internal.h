@@ -78,6 +78,7 @@ __host__ __device__ inline double* muon_partials(uint8_t* ws) { return reinterpr
 // Small calls of the iterate kernel: tiles of 128 rows x 64 columns, only those that hold rows and
 // columns of the matrix (its rows and the columns of A and B in whole 128s: they are K elements).
 constexpr int kMuonSmallUnits = 296;    // most units of a product, two for each of 148 SMs
+constexpr int kMuonSmallSteps = 3500;   // most K steps of an update
 __host__ __device__ inline int32_t muon_steps(int32_t k) { return (k + 63) / 64; }
 __host__ __device__ inline int32_t muon_row_tiles(int32_t m) { return (m + 127) / 128; }
 // Tiles of A or B from the diagonal's 256-blocks on.

@@ -406,7 +406,12 @@ int splits_of(int64_t tiles, int kt, int64_t slots) {
 }  // namespace
 
 cudaError_t launch_mxfp4_gemm(const MxGemmArgs& g, cudaStream_t st, int num_sms) {
-  if (g.M > 64 && g.N > 64 && ((g.M + 255) / 256) * ((g.N + 255) / 256) >= 40) return launch_mxfp4_pair(g, st);
+  // CTA pairs from the point on where 256 x 256 tiles keep enough of them busy; with a long K and few
+  // tiles, splitting K does more.  Both sides (us, tile kernel and pairs): 256 x 8192 x 8192 (32 tiles)
+  // 21.0 and 17.8, 768 x 2048 x 2048 (24) 10.7 and 9.8, 1024 x 1024 x 512 (16) 9.2 and 7.8, 1024 x 1024
+  // x 16384 (16) 22.7 and 27.1, 128 x 8192 x 8192 (32, half empty) 15.2 and 17.4.
+  const int64_t tiles256 = ((g.M + 255) / 256) * ((g.N + 255) / 256);
+  if (g.M > 128 && g.N > 128 && tiles256 >= (g.K <= 2048 ? 16 : 24)) return launch_mxfp4_pair(g, st);
   TileArgs a{};
   // the narrow side: A's rows when they are at most 64 and no more than B's
   const bool swap = g.M <= 64 && g.M <= g.N;
