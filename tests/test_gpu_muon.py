@@ -183,6 +183,35 @@ def test_streams_and_graphs(fs4):
         assert all(torch.equal(a, b) for a, b in zip(W + M, W2 + M2))
 
 
+def test_two_steps_at_once_with_workspaces_of_their_own(fs4):
+    """Steps of both kernel kinds on two streams, none waiting for the other."""
+    shapes = [(900, 1400), (64, 200), (20, 900), (2048, 2304)]
+    Gs = [make(*s, torch.bfloat16).cuda() for s in shapes]
+    want = [fs4.muon_orthogonalize([G])[0] for G in Gs]
+    spaces = [torch.empty(fs4.muon_workspace_size([s]), dtype=torch.uint8, device="cuda") for s in shapes]
+    streams = [torch.cuda.Stream() for _ in shapes]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(6):
+        for G, ws, st in zip(Gs, spaces, streams):
+            outs.append(fs4.muon_orthogonalize([G], workspace=ws, stream=st)[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i % len(shapes)]) for i, o in enumerate(outs))
+    assert all(fs4.device_status(ws) == 0 for ws in spaces)
+
+
+def test_large_batch_takes_the_whole_table(fs4):
+    """More matrices than the small parameter block holds, thin and wide ones mixed."""
+    shapes = [(1 + 37 * i % 90, 1 + 53 * i % 310) for i in range(224)]
+    Gs = [make(*s).cuda() for s in shapes]
+    outs = fs4.muon_orthogonalize(Gs, K=3)
+    for i in (0, 7, 100, 150, 223):
+        assert torch.equal(outs[i], fs4.muon_orthogonalize([Gs[i]], K=3)[0])
+        assert far(outs[i], O.orthogonalize(np64(Gs[i]), 3)) <= NEAR + half_step(torch.bfloat16)
+    with pytest.raises(fs4.Fs4Error):
+        fs4.muon_orthogonalize(Gs + Gs[:1])
+
+
 def test_refusals_on_device(fs4):
     G, W = torch.zeros(8, 16, device="cuda"), torch.zeros(8, 16, device="cuda")
     with pytest.raises(ValueError):

@@ -194,6 +194,35 @@ def test_calls_repeat_bit_for_bit_on_streams_and_in_graphs(fs4):
     assert torch.equal(out, fs4.mxfp4_linear(x, w, 400))
 
 
+def test_products_at_once_share_a_status_word(fs4):
+    """Large and small products on two streams with one workspace, which only holds the status."""
+    (a, _), (b, _) = operand(fs4, 1300, 512, 1), operand(fs4, 1500, 512, 2)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    want = [fs4.mxfp4_gemm(a, b, M, 1500, 512) for M in (1300, 3, 100)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [(i, fs4.mxfp4_gemm(a, b, M, 1500, 512, workspace=ws, stream=s)) for _ in range(5) for s in (side, None)
+            for i, M in enumerate((1300, 3, 100))]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i, o in outs) and fs4.device_status(ws) == 0
+
+
+def test_linear_follows_its_operands_producers_without_a_sync(fs4):
+    """Each call's x is written by the launch before it, in one workspace for all."""
+    w = fs4.mxfp4_quantize(make(600, 1024, torch.float32, 4).cuda(), tiled=True)
+    for M in (1, 5, 40, 1500):
+        base = make(M, 1024, torch.bfloat16).cuda()
+        want = [fs4.mxfp4_linear((base * k), w, 600) for k in range(8)]
+        torch.cuda.synchronize()
+        ws = torch.zeros(fs4.mxfp4_linear_workspace_size(M, 1024), dtype=torch.uint8, device="cuda")
+        x, outs = torch.empty_like(base), []
+        for k in range(8):
+            torch.mul(base, k, out=x)
+            outs.append(fs4.mxfp4_linear(x, w, 600, workspace=ws))
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, t) for o, t in zip(outs, want))
+
+
 def test_three_products_of_a_linear_layer(fs4):
     """y = x W^T, dx = dy W, dW += dy^T x on quantised operands, against the oracle's operands."""
     T, n_in, n_out = 200, 300, 170
