@@ -556,14 +556,32 @@ __device__ __forceinline__ bool multiply(const MuonCall& p, Shared& sh, Ring<kPa
       if (!landed) return false;
       tc_fence_after();
       const bool am = k < a_turn, bm = k < b_turn;
-      // 16 k: 32 bytes along a row, or 16 rows of 128 bytes
-      const uint64_t da = (am ? ca0 : ra0) + ring.s * kStep, db = (bm ? cb0 : rb0) + ring.s * kStep;
-      const uint64_t ia = am ? 128 : 2, ib = bm ? 128 : 2;
-      const uint32_t idesc = idesc_f16(kPair ? 256 : 128, T::kN, am, bm);
+      // (constant steps and instruction descriptors: every value computed here is an issue slot more)
+      auto issue = [&](auto am_c, auto bm_c) {
+        constexpr int kAm = decltype(am_c)::value, kBm = decltype(bm_c)::value;
+        // 16 k: 32 bytes along a row, or 16 rows of 128 bytes
+        const uint64_t da = (kAm ? ca0 : ra0) + ring.s * kStep, db = (kBm ? cb0 : rb0) + ring.s * kStep;
+        constexpr uint64_t ia = kAm ? 128 : 2, ib = kBm ? 128 : 2;
+        constexpr uint32_t idesc = idesc_f16(kPair ? 256 : 128, T::kN, kAm, kBm);
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        if constexpr (kPair) tc_mma_f16_pair(acc, da + h * ia, db + h * ib, idesc, (i | h) != 0 ? 1u : 0u);
-        else tc_mma_bf16(acc, da + h * ia, db + h * ib, idesc, (i | h) != 0 ? 1u : 0u);   // kind::f16: the type is in idesc
+        for (int h = 0; h < 4; ++h) {
+          const uint32_t acc_on = h != 0 ? 1u : (i != 0 ? 1u : 0u);
+          if constexpr (kPair) tc_mma_f16_pair(acc, da + h * ia, db + h * ib, idesc, acc_on);
+          else tc_mma_bf16(acc, da + h * ia, db + h * ib, idesc, acc_on);   // kind::f16: the type is in idesc
+        }
+      };
+      using No = std::integral_constant<int, 0>;
+      using Yes = std::integral_constant<int, 1>;
+      if constexpr (E == kGram) {
+        issue(No{}, No{});
+      } else if constexpr (E == kUpdate) {
+        if (am) issue(Yes{}, Yes{});
+        else issue(No{}, Yes{});
+      } else {
+        if (am && bm) issue(Yes{}, Yes{});
+        else if (am) issue(Yes{}, No{});
+        else if (bm) issue(No{}, Yes{});
+        else issue(No{}, No{});
       }
       if constexpr (kPair) tc_commit_pair(&sh.empty[ring.s]);
       else tc_commit(&sh.empty[ring.s]);
