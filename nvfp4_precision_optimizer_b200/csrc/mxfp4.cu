@@ -16,8 +16,10 @@
 // One pass: each CTA reads a 128 x 128 tile once (four pieces of sixteen elements a thread, all
 // loads first, two threads a 32-element block) and writes the row view from registers; the column view
 // reads the tile back from shared memory, one thread a column (FP32) or a pair of columns
-// (16-bit types), and both views' scales leave as whole 512-byte atoms.  Bound by HBM: in
-// bytes per element the input's size plus 17/32 for each view.
+// (16-bit types), and both views' scales leave as whole 512-byte atoms.  The floor is HBM: in
+// bytes per element the input's size plus 17/32 for each view.  Measured on BF16: the row view of
+// 8192 x 4096 20 us (4.3 TB/s), both views of 8192 x 5120 42 us (3.1 TB/s); stochastic 98 us, where
+// the random stream's arithmetic keeps 67% of the issue slots busy.
 #include <cstdint>
 #include <type_traits>
 
@@ -379,7 +381,8 @@ struct MxDequantArgs {
 };
 
 // y = code 2^(byte - 127), rounded once to T.  Eight elements a thread, 256 columns a warp,
-// four rows a warp at once so that four loads are in flight.  Bound by HBM.
+// four rows a warp at once so that four loads are in flight.  Bound by HBM: 8192 x 5120 to BF16
+// 21.6 us, 4.9 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(kMxThreads) mxfp4_dequantize_kernel(const __grid_constant__ MxDequantArgs a) {
   __shared__ __align__(16) float turn[kMxThreads / 32][256];

@@ -9,6 +9,11 @@
 namespace fs4 {
 namespace {
 
+// Few rows or small products are bound by latency and by the weights' bytes: 1 x 28672 x 8192 reads
+// them at 5.1 TB/s (24.8 us), 1 x 8192 x 8192 takes 11.5 us of which about 5.6 do not depend on the
+// size, 250 x 512 x 640 takes 8 us.  Splitting K over a cluster fills the device where tiles are few;
+// its CTAs add their partial tiles up through shared memory, in rank order.
+//
 // One 128 x TN tile of D^(T) per CTA, K split over the CTAs of a cluster.  The operand on the
 // tensor core's 128-row side is P, the one on its TN-row side Q; with few rows of A (decoding)
 // P = B, so that the weights fill the tensor core and the tokens are its narrow side.

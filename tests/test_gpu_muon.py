@@ -93,6 +93,18 @@ def test_strided_inputs_and_outputs(fs4):
         assert torch.equal(wide[:, 4:-5], want) and (wide[:, :4] == 3).all() and (wide[:, -5:] == 3).all()
 
 
+@pytest.mark.parametrize("shape", [(1, 300), (20, 77), (77, 20), (300, 411), (411, 300), (1500, 1900), (1900, 1501)], ids=str)
+def test_rows_past_the_weights_and_momenta_stay_as_they_are(fs4, shape):
+    m, n = shape
+    G = make(m, n).cuda()
+    W, M = (torch.full((m + 3, n), 5.0, device="cuda") for _ in range(2))
+    w, v = torch.full((m, n), 5.0, device="cuda"), torch.full((m, n), 5.0, device="cuda")
+    fs4.muon_step([W[1:m + 1]], [G], [M[1:m + 1]], lr=0.1, weight_decay=0.1)
+    fs4.muon_step([w], [G], [v], lr=0.1, weight_decay=0.1)
+    for big, one in ((W, w), (M, v)):
+        assert torch.equal(big[1:m + 1], one) and (big[0] == 5).all() and (big[m + 1:] == 5).all()
+
+
 def test_zero_tiny_and_huge_updates(fs4):
     G = make(60, 90)
     want = fs4.muon_orthogonalize([G.cuda()])[0]

@@ -60,12 +60,12 @@ def test_quantize_extremes(fs4, kind):
     x[2, 32:40] = torch.tensor([6.0, 5.0, 3.5, 2.5, 1.75, 1.25, 0.75, 0.25]).to(t)
     x[3, 64:67] = torch.tensor([f.tiny / 4, -f.tiny / 2, f.tiny / 8]).to(t)
     x[4, 3], x[4, 40], x[5, 95] = float("nan"), float("inf"), float("-inf")
-    for seed in (None, 3):
-        row, col = fs4.mxfp4_quantize_both(x.cuda(), seed=seed)
-        same(row, O.quantize(np64(x), "floor", seed), False)
-        same(col, O.quantize(np64(x).T, "floor", None if seed is None else seed ^ O.COLUMN_SEED), False)
+    for seed, rule in ((None, "floor"), (3, "floor"), (None, "ceil"), (3, "ceil")):
+        row, col = fs4.mxfp4_quantize_both(x.cuda(), seed=seed, scale_rule=rule)
+        same(row, O.quantize(np64(x), rule, seed), False)
+        same(col, O.quantize(np64(x).T, rule, None if seed is None else seed ^ O.COLUMN_SEED), False)
         y = fs4.mxfp4_dequantize(*row, 6, 96, dtype=t).cpu()
-        want = O.values(*O.quantize(np64(x), "floor", seed))
+        want = O.values(*O.quantize(np64(x), rule, seed))
         with np.errstate(over="ignore"):
             assert torch.equal(torch.nan_to_num(y, nan=1.5), torch.nan_to_num(torch.from_numpy(want).to(t), nan=1.5))
             assert (torch.isnan(y).numpy() == np.isnan(want)).all()
@@ -142,7 +142,17 @@ def test_gemm_against_float64(fs4, size, kind):
     assert fs4.device_status(ws) == 0
 
 
-@pytest.mark.parametrize("size", [(1, 256, 512), (40, 130, 300), (300, 140, 300)], ids=str)
+@pytest.mark.parametrize("size", [(1, 200, 512), (17, 130, 300), (140, 150, 300), (1300, 1500, 256), (1300, 1501, 256)], ids=str)
+def test_rows_and_columns_past_the_product_stay_as_they_are(fs4, size):
+    M, N, K = size
+    (a, _), (b, _) = operand(fs4, M, K, 1), operand(fs4, N, K, 2)
+    want = fs4.mxfp4_gemm(a, b, M, N, K)
+    big = torch.full((M + 3, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    fs4.mxfp4_gemm(a, b, M, N, K, out=big[1:M + 1])
+    assert torch.equal(big[1:M + 1], want) and (big[0] == 5).all() and (big[M + 1:] == 5).all()
+
+
+@pytest.mark.parametrize("size", [(1, 256, 512), (40, 130, 300), (300, 140, 300), (1500, 1400, 300)], ids=str)
 def test_gemm_nan_blocks_reach_their_rows_and_no_others(fs4, size):
     M, N, K = size
     x = make(M, K, torch.float32)
