@@ -597,6 +597,18 @@ __device__ __forceinline__ bool multiply(const MuonCall& p, Shared& sh, Ring<kPa
   return true;
 }
 
+// The small variant's eight epilogue warps: true if it is true in all of them.
+__device__ __forceinline__ bool vote(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+
 // A split product's unit: leave this part's sums in the workspace; the CTA that finishes a tile's
 // last part adds all parts up, in their order, into `v` and returns true.
 __device__ __forceinline__ bool sum_parts(const MuonCall& p, Shared& sh, const Job& j, int32_t u, uint32_t taddr, int quad_, int half,
@@ -639,35 +651,35 @@ __device__ __forceinline__ bool sum_parts(const MuonCall& p, Shared& sh, const J
 
 template <bool kPair, int E, bool kLast>
 __device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, Deal<kPair>& deal, uint32_t& tl, int it, uint32_t tmem, uint32_t rank, int quad_,
-                                       int half, int lane, volatile int* abort) {
+                                       int half, int lane, volatile int* abort, bool alive) {
   using T = Tile<kPair>;
   const int32_t total = sh.prefix[E][p.count];
   int seen = -1;
+  bool ok = kPair || alive;
   for (int32_t u = deal.next; u < total; u += deal.step(), ++tl) {
     const Job j = make_job<kPair, E>(p, sh, u, rank);
     const uint32_t b = tl & 1u;
     const Place<kPair, E> w(p, sh, j, it, quad_, half, lane);
     float* diag = sh.diag[4 * half + quad_];
     // other CTAs' results are read below: see them
-    bool ok = true;
-    if (j.mat != seen && (E != kGram || it > 0)) {
+    if (ok && j.mat != seen && (E != kGram || it > 0)) {
       if (lane == 0) ok = wait_count(muon_counts(p.ws) + j.mat, units_before<kPair, E>(sh, j.mat, it), muon_status(p.ws), abort);
       ok = __all_sync(0xFFFFFFFFu, ok);
       seen = j.mat;
     }
-    if ((kPair || E != kGram) && !ok) return false;
+    if (kPair && !ok) return false;
     Ahead a;
     look_ahead<kPair, E, kLast>(p, w, a, diag, it, lane);
     if (ok && lane == 0) ok = mbar_wait(&sh.acc_full[b], (tl >> 1) & 1u, muon_status(p.ws), abort);
     ok = __all_sync(0xFFFFFFFFu, ok);
-    if (!kPair && E == kGram) {
-      // the warps meet in split units: all go on, or none
-      if (!ok && lane == 0) *abort = 1;
-      named_bar(2, 256);
-      ok = *abort == 0;
-      named_bar(2, 256);
+    // The small variant's warps meet in split units: all of them work there or none. A vote, not
+    // the flag, which another warp may raise between two warps' reads; and a warp whose wait ran
+    // out stays, without work, so that it is there for the votes that follow.
+    if (!kPair && E == kGram && j.parts > 1) ok = vote(ok);
+    if (!ok) {
+      if (kPair) return false;
+      continue;
     }
-    if (!ok) return false;
     __syncwarp();
     tc_fence_after();
     const uint32_t taddr = tmem + (uint32_t)T::kN * b + ((uint32_t)(32 * quad_) << 16) + (uint32_t)(T::kWarpCols * half);
@@ -689,7 +701,7 @@ __device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, Deal<kPair
     }
   }
   deal.skip(total);
-  return true;
+  return ok;
 }
 
 template <bool kPair>
@@ -780,12 +792,12 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
     Deal<kPair> deal;
     uint32_t tl = 0;
     bool ok = true;
-    for (int ph = 0; ph < 3 * p.K && ok; ++ph) {
+    for (int ph = 0; ph < 3 * p.K && (ok || !kPair); ++ph) {
       const int it = ph / 3, e = ph - 3 * it;
-      ok = e == kGram ? finish<kPair, kGram, false>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort)
-           : e == kSquare ? finish<kPair, kSquare, false>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort)
-           : it < p.K - 1 ? finish<kPair, kUpdate, false>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort)
-                          : finish<kPair, kUpdate, true>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort);
+      ok = e == kGram ? finish<kPair, kGram, false>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort, ok)
+           : e == kSquare ? finish<kPair, kSquare, false>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort, ok)
+           : it < p.K - 1 ? finish<kPair, kUpdate, false>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort, ok)
+                          : finish<kPair, kUpdate, true>(p, sh, deal, tl, it, tmem, rank, quad_, half, lane, abort, ok);
     }
   }
   __syncwarp();
