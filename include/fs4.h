@@ -508,12 +508,15 @@ fs4_status fs4_root_ns_bf16_batched_timed(int32_t count, const fs4_ns_desc* desc
  * The Newton-Schulz step of Section 2 "Root optimizer" at working precision, as the Muon
  * optimizer takes it, for matrices of any size in [1, FS4_MAX_DIM]^2: no quantisation and no
  * clip.  Where fs4_root_ns and fs4_root_ns_bf16_batched trade accuracy for 4-bit or BF16
- * operands, this step is meant to be exact to the BF16 rounding of its result:
+ * operands, this step is meant to be about as exact as BF16 holds its result:
  *   X_0 = U / (||U||_F + 1e-7) (transposed when rows > cols), then K times
  *   A = X X^T, B = b A + c A^2, X <- a X + B X,
  * with FP16 tensor-core operands, FP32 accumulation and FP32 diagonals of A and B kept out
- * of the operands.  With the Muon coefficients and K = 5 the result is 0.3-1.3e-3 (relative,
- * Frobenius) from the exact iteration; it repeats bit for bit.  A zero matrix gives zero.  A
+ * of the operands.  With the Muon coefficients and K = 5 the result is 0.1-1.8e-3 (relative,
+ * Frobenius) from the exact iteration, also where a few directions dominate and the rest is
+ * 1e-5 of them.  It is up to 1.2e-2 where the elements of one dominant direction are all equal
+ * (equal elements round alike, where others average out), and about 3e-3 for K = 10, since the
+ * Muon iteration does not converge.  The result repeats bit for bit.  A zero matrix gives zero.  A
  * matrix with NaN or Inf in U is carried as zeros (its update is zero) and recorded as
  * FS4_ERR_NONFINITE in the status word; so is a result that is not finite, as coefficients
  * that make the iteration diverge give. */

@@ -429,7 +429,8 @@ def muon_orthogonalize(Gs: Sequence[torch.Tensor], K: int = 5, coeffs=MUON_COEFF
                        outs: Sequence[torch.Tensor] | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Orthogonalise a list of FP32, BF16 or FP16 matrices of any sizes by K Newton-Schulz
     iterations (fs4_muon_orthogonalize), in `dtype` or into `outs`.  coeffs is one (a, b, c)
-    or one per iteration.  Accurate to BF16: about 1e-3 of the exact iteration."""
+    or one per iteration.  About 1e-3 from the exact iteration, at most 2e-3 but for dominant
+    directions of equal elements (include/fs4.h)."""
     if not Gs:
         return []
     dev = Gs[0].device

@@ -9,9 +9,18 @@
 // error of the step.  The diagonals stay in FP32 and out of the operands:
 //   A = A0 + D:  A^2 = A0^2 + A0 D + D A0 + D^2,   element ij: (A0^2)_ij + A0_ij (d_i + d_j), d_i^2 on the diagonal
 //   B = B0 + E:  a X + B X = (a + e_i) X_ij + (B0 X)_ij
-// which the epilogues add from the FP32 diagonals.  Measured on Gaussian and low-rank inputs
-// (numpy, 256^2 to 768 x 2048): 0.4-1.3e-3 from the exact iteration after five steps, against
-// 2.6e-3 with rounded diagonals and 1.4-2.4e-2 with BF16 operands.
+// which the epilogues add from the FP32 diagonals.  The tensor cores multiply B0 by X's high part
+// alone, so with X = H + L the update leaves out B0 L.  Where one direction dominates, B L lies in
+// that direction and does no harm, but B0 L = B L - E L does not: E L reaches the small singular
+// values, which the iterations left raise by a factor a each.  So all but the last two updates
+// apply E to H as well (what is left out is then B L):
+//   X' = (a + e_i) H_ij + a L_ij + (B0 H)_ij
+// and the last two, where nothing small is left to raise and B is nearly diagonal, apply it to H + L.
+// Restated in numpy (K = 5, 33 to 1024 rows): Gaussian, decaying and low-rank inputs and up to 1e-5
+// of noise beside a few dominant directions 0.1-1.8e-3 from the exact iteration, against up to 4e-2
+// with E applied to H + L throughout (and up to 1e-1 with K = 10).  Rounded diagonals give 2.6e-3
+// and BF16 operands 1.4-2.4e-2 on Gaussian inputs.  A dominant direction whose elements are all
+// equal is the worst case, since equal elements round alike: up to 1.2e-2.
 // A and B are symmetric: only 256 x 256 blocks on and above the diagonal are computed and
 // stored.  A block below it is read as its mirror image with the operand's M or N index
 // fastest, which the tensor core takes directly; so is X as the second operand of the update,
@@ -357,6 +366,7 @@ struct Place {
 struct Ahead {
   Input in[2];
   float own;             // d_i (Square) or a + e_i (Update)
+  float own_low;         // Update: what multiplies X's low part, a or a + e_i
 };
 template <bool kPair, int E, bool kLast>
 __device__ __forceinline__ void look_ahead(const MuonCall& p, const Place<kPair, E>& w, Ahead& a, float* diag, int it, int lane) {
@@ -370,7 +380,9 @@ __device__ __forceinline__ void look_ahead(const MuonCall& p, const Place<kPair,
     else diag[lane] = __ldcg(w.da + w.col0 + lane);
     __syncwarp();
   } else {
-    a.own = p.coeffs[p.n_coeffs == 1 ? 0 : 3 * it] + __ldcg(w.db + w.row);
+    const float pa = p.coeffs[p.n_coeffs == 1 ? 0 : 3 * it];
+    a.own = pa + __ldcg(w.db + w.row);
+    a.own_low = it >= p.K - 2 ? a.own : pa;
   }
 }
 
@@ -419,9 +431,10 @@ __device__ __forceinline__ void epilogue(const MuonCall& p, const Place<kPair, E
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float* y = v + 8 * q;
-        float x[8];
-        join8(quad(ordered(in.h[q >> 1], w.swap), q & 1), quad(ordered(in.l[q >> 1], w.swap), q & 1), x);
+        const uint4 hi = quad(ordered(in.h[q >> 1], w.swap), q & 1), lo = quad(ordered(in.l[q >> 1], w.swap), q & 1);
         if constexpr (E == kSquare) {
+          float x[8];
+          join8(hi, lo, x);
           const float4 d0 = reinterpret_cast<const float4*>(diag + c)[2 * q], d1 = reinterpret_cast<const float4*>(diag + c)[2 * q + 1];
           const float dc[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
           if (on) {
@@ -433,9 +446,14 @@ __device__ __forceinline__ void epilogue(const MuonCall& p, const Place<kPair, E
 #pragma unroll
           for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], fmaf(pc, a.own + dc[i], pb), y[i] * (pc / kAScale));
         } else {
-          // kXScale times (a + e_i) X + B0 X
+          // kXScale times (a + e_i) H + (a or a + e_i) L + B0 H
+          const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+          const float own_low = kLast ? a.own : a.own_low;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = fmaf(a.own, x[i], y[i] * (1.0f / kAScale));
+          for (int i = 0; i < 4; ++i) {
+            y[2 * i] = fmaf(a.own, half_lo(h[i]), fmaf(own_low, half_lo(l[i]), y[2 * i] * (1.0f / kAScale)));
+            y[2 * i + 1] = fmaf(a.own, half_hi(h[i]), fmaf(own_low, half_hi(l[i]), y[2 * i + 1] * (1.0f / kAScale)));
+          }
         }
       }
       if (E == kSquare && on) {

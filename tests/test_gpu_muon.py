@@ -269,3 +269,49 @@ def test_training_step_in_four_bits(fs4):
     assert np.linalg.norm(np64(w) - moved) <= (NEAR + 2.0 ** -15) * np.linalg.norm(moved - W0) + 2.0 ** -23 * np.linalg.norm(moved)
     codes, scales = MX.pack_tiled(*MX.quantize(np64(w)))
     assert np.array_equal(wr2[0].cpu().numpy(), codes) and np.array_equal(wr2[1].cpu().numpy(), scales)
+
+
+def dominated(m, n, kind, noise):
+    """One or few dominant directions over `noise` times as much noise an element."""
+    g = torch.Generator().manual_seed(31 * m + n)
+    rand = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    if kind == "few rows":
+        x = noise * rand(m, n)
+        x[:5] += rand(5, 1) @ rand(1, n)
+        return x
+    if kind == "one row above all":          # three quarters of the direction in one row
+        u = rand(m, 1)
+        u[0] = 0
+        u *= 0.5 / u.norm()
+        u[0] = 0.75 ** 0.5
+        return (u @ rand(1, n) + noise * rand(m, n) * m ** -0.5)
+    if kind == "fading rows":
+        return 0.6 ** torch.arange(m, dtype=torch.float64)[:, None] @ rand(1, n) + noise * rand(m, n)
+    return rand(m, 4 if kind == "rank 4" else 1) @ rand(4 if kind == "rank 4" else 1, n) + noise * rand(m, n)
+
+
+@pytest.mark.parametrize("noise", (1e-2, 1e-3, 1e-4))
+@pytest.mark.parametrize("kind", ("rank 1", "rank 4", "few rows", "one row above all", "fading rows"))
+@pytest.mark.parametrize("shape", [(40, 300), (64, 64), (128, 128), (411, 300), (2000, 1400)], ids=str)
+def test_dominant_directions_leave_the_small_ones_exact(fs4, shape, kind, noise):
+    """The iteration raises small singular values up to a^5 = 485 times, and so an error that
+    the dominant ones leave among them.  The contract's bound, on both kernels."""
+    G = dominated(*shape, kind, noise).float()
+    got = fs4.muon_orthogonalize([G.cuda()], dtype=torch.float32)[0]
+    if G.numel() < 1 << 20:
+        assert far(got, O.orthogonalize(np64(G))) <= NEAR
+    else:
+        x = G.cuda().double()
+        x = x.T / (x.norm() + 1e-7)
+        for _ in range(5):
+            a = x @ x.T
+            x = O.MUON[0] * x + (O.MUON[1] * a + O.MUON[2] * (a @ a)) @ x
+        assert far(got, np64(x.T)) <= NEAR
+
+
+@pytest.mark.parametrize("shape", [(64, 64), (200, 200), (300, 40)], ids=str)
+def test_converging_iterations_keep_small_directions(fs4, shape):
+    G = dominated(*shape, "rank 1", 1e-3).float()
+    per = (1.875, -1.25, 0.375)
+    got = fs4.muon_orthogonalize([G.cuda()], K=20, coeffs=per, dtype=torch.float32)[0]
+    assert far(got, O.orthogonalize(np64(G), 20, per)) <= NEAR
