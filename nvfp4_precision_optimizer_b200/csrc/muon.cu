@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2) muon_prepare_kernel(const __grid_
       for (int i = threadIdx.x; i < d.parts; i += kThreads) s += part[i];
       s = block_sum(s, red);
       const bool fine = isfinite(s);
-      inv = fine ? (float)(1.0 / (sqrt(s) + 1e-7)) * kXScale : -1.0f;   // -1: carried as zeros
+      inv = fine ? (float)(kXScale / (sqrt(s) + 1e-7)) : -1.0f;   // -1: carried as zeros
       if (!fine && threadIdx.x == 0) atomicOr(muon_status(p.ws), kStatusNonFinite);
     }
     const int32_t tu = u - prefix[mi], across = d.np / 64;

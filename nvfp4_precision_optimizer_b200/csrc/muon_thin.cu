@@ -150,9 +150,12 @@ __global__ void __launch_bounds__(1024) muon_thin_iterate_kernel(const __grid_co
     }
     __syncthreads();
   }
-  if (mine) reinterpret_cast<float*>(ws)[threadIdx.x] = fine ? (float)T[i][j] : 0.0f;
+  // T holds 1 / ||U||: beside a norm near FP32's largest values U is taken times 2^-64 and T times
+  // 2^64, which keeps T a normal number
+  const double shift = inv < 0x1p-100 ? 0x1p-64 : 1.0;
+  if (mine) reinterpret_cast<float*>(ws)[threadIdx.x] = fine ? (float)(T[i][j] / shift) : 0.0f;
   if (threadIdx.x == 0) {
-    *reinterpret_cast<float*>(ws + thin_flag_offset(m)) = fine ? 1.0f : 0.0f;
+    *reinterpret_cast<float*>(ws + thin_flag_offset(m)) = fine ? (float)shift : 0.0f;
     if (!fine) atomicOr(muon_status(p.ws), kStatusNonFinite);
   }
 }
@@ -170,12 +173,15 @@ __global__ void __launch_bounds__(kThreads) muon_thin_apply_kernel(const __grid_
     const int i = e / kMuonThin, j = e % kMuonThin;
     T[i][j] = (i < m && j < m) ? reinterpret_cast<const float*>(ws)[i * m + j] : 0.0f;
   }
-  const bool fine = *reinterpret_cast<const float*>(ws + thin_flag_offset(m)) != 0.0f;
+  const float shift = *reinterpret_cast<const float*>(ws + thin_flag_offset(m));
+  const bool fine = shift != 0.0f;
   float u[kMuonThin];
 #pragma unroll
   for (int r = 0; r < kMuonThin; r += 8) {
     if (r < m) {
       direction_column8(p, d, r, c, u + r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[r + i] *= shift;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[r + i] = 0.0f;

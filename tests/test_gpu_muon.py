@@ -315,3 +315,19 @@ def test_converging_iterations_keep_small_directions(fs4, shape):
     per = (1.875, -1.25, 0.375)
     got = fs4.muon_orthogonalize([G.cuda()], K=20, coeffs=per, dtype=torch.float32)[0]
     assert far(got, O.orthogonalize(np64(G), 20, per)) <= NEAR
+
+
+@pytest.mark.parametrize("shape", [(20, 90), (1, 33), (90, 64), (300, 411)], ids=str)
+def test_updates_near_the_largest_fp32_values(fs4, shape):
+    """1 / ||U|| is not a normal FP32 number from a norm of 2^126 on; a power of two on U is exact."""
+    G = make(*shape)
+    G = G / G.abs().max()
+    want = fs4.muon_orthogonalize([G.cuda() * 2.0 ** 20], dtype=torch.float32)[0]
+    for scale in (2.0 ** 110, 2.0 ** 124, 2.0 ** 127):
+        got = fs4.muon_orthogonalize([(G * scale).cuda()], dtype=torch.float32)[0]
+        # T or X_0 is rounded to FP32 once, wherever the power of two is
+        assert far(got, np64(want)) <= 2.0 ** -20, scale
+        w = torch.zeros(shape, device="cuda")
+        m = torch.zeros(shape, device="cuda")
+        fs4.muon_step([w], [(G * scale).cuda()], [m], lr=1.0, beta=0.0, nesterov=False, scale=1.0)
+        assert torch.equal(w, -got)
