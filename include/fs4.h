@@ -541,8 +541,11 @@ typedef struct {
 size_t fs4_muon_workspace_size(int32_t count, const int64_t* rows, const int64_t* cols);
 
 /* w = scale X_K of U = g for every matrix (descs: HOST array), in three launches over all of
- * them (three more for matrices with 32 rows or columns or fewer).  coeffs: HOST array of n_coeffs triples (a, b, c), one for all iterations or one for
- * each (n_coeffs = 1 or K); |a|, |b|, |c| <= 16.
+ * them (three more for matrices with 32 rows or columns or fewer).  coeffs: HOST array of n_coeffs
+ * triples (a, b, c), one for all iterations or one for each (n_coeffs = 1 or K), with |a| <= 16 and
+ * |b s + c s^2| <= 255 for 0 <= s <= 1 (s: a squared singular value).  Where an iterate leaves the
+ * range of the FP16 operands all the same (an element of X of 16, one of A or B of 255), the result
+ * is not finite.
  *   Errors: FS4_ERR_SHAPE (count outside [1, FS4_MAX_BATCH], K outside [1, FS4_MAX_ITERS], a
  *   size), FS4_ERR_INVALID_ARG (null or misaligned pointers, leading dimensions, types,
  *   coefficients, scale), FS4_ERR_ALIAS (an output overlaps an input, another output or the

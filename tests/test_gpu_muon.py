@@ -331,3 +331,26 @@ def test_updates_near_the_largest_fp32_values(fs4, shape):
         m = torch.zeros(shape, device="cuda")
         fs4.muon_step([w], [(G * scale).cuda()], [m], lr=1.0, beta=0.0, nesterov=False, scale=1.0)
         assert torch.equal(w, -got)
+
+
+@pytest.mark.parametrize("shape", [(64, 64), (200, 310), (1500, 1900), (20, 500)], ids=str)
+def test_steep_first_triples(fs4, shape):
+    """A schedule whose first triples have large b and c, as those that converge fastest do.  It
+    raises small singular values 1000 times, where the Muon triple raises them 485 times: twice
+    the bound."""
+    per = [(8.16, -22.5, 15.9), (4.1, -2.95, 0.545), (3.95, -2.91, 0.552), (3.3, -2.49, 0.51), (2.3, -1.67, 0.42)]
+    ws = torch.empty(fs4.muon_workspace_size([shape]), dtype=torch.uint8, device="cuda")
+    G = make(*shape)
+    got = fs4.muon_orthogonalize([G.cuda()], coeffs=per, dtype=torch.float32, workspace=ws)[0]
+    assert far(got, O.orthogonalize(np64(G), 5, per)) <= 2 * NEAR and fs4.device_status(ws) == 0
+
+
+def test_iterates_that_leave_the_operands_range_are_reported(fs4):
+    """One element of 16 in X (a = 16 on a matrix of one element), and a B over 255."""
+    G = torch.zeros(64, 64, device="cuda")
+    G[3, 5] = 2.0
+    ones = torch.ones(64, 64, device="cuda")
+    for x, per in ((G, [(16.0, 0.0, 0.0), (1.0, 0.0, 0.0)]), (ones, [(16.0, 16.0, 16.0), (16.0, 16.0, 16.0)])):
+        ws = torch.empty(fs4.muon_workspace_size([(64, 64)]), dtype=torch.uint8, device="cuda")
+        fs4.muon_orthogonalize([x], K=len(per), coeffs=per, workspace=ws)
+        assert fs4.device_status(ws) == -7

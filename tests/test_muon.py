@@ -105,3 +105,21 @@ def test_binding_refusals(F):
     assert F.muon_orthogonalize([]) == []
     assert F._muon_scale("spectral", 8, 2) == 2.0 and F._muon_scale("spectral", 2, 8) == 1.0
     assert F._muon_scale("rms", 25, 4) == 1.0 and F._muon_scale(3, 1, 1) == 3.0
+
+
+def test_coefficient_ranges(F):
+    """|a| <= 16 and |b s + c s^2| <= 255 on [0, 1]: accepted triples get as far as the workspace."""
+    size = F.muon_workspace_size([(32, 48)])
+
+    def call(*triples):
+        d = (F._lib.MuonDesc * 1)(_desc(F, 1 << 32, step=False))
+        flat = [v for t in triples for v in t]
+        return F._lib.lib().fs4_muon_orthogonalize(1, d, len(triples), (ctypes.c_float * len(flat))(*flat), len(triples),
+                                                   1 << 40, size - 1, None)
+
+    steep = (8.16, -22.5, 15.9)
+    for ok in (O.MUON, steep, (16.0, 16.0, 16.0), (-16.0, 0.0, 255.0), (1.0, 1000.0, -1000.0), (0.0, -255.0, 0.0), (1.0, -31.0, 1.0)):
+        assert call(ok) == -4 and call(steep, ok) == -4, ok
+    for bad in ((16.5, 0, 0), (1, 256, 0), (1, 0, -256), (1, 1100, -1100), (1, float("inf"), 0), (1, 0, float("nan")),
+                (1, 3e38, -3e38), (float("-inf"), 0, 0)):
+        assert call(bad) == -1 and call(steep, bad) == -1, bad
