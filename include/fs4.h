@@ -560,7 +560,7 @@ fs4_status fs4_muon_orthogonalize(int32_t count, const fs4_muon_desc* descs, int
  *   m <- beta m + (1 - beta) g         (in FP32, rounded to m's type)
  *   U = m, or with FS4_MUON_NESTEROV  beta m + (1 - beta) g  from the stored m
  *   w <- (1 - lr weight_decay) w - lr scale X_K      (in FP32, rounded to w's type)
- * lr >= 0, 0 <= beta < 1.  Errors as fs4_muon_orthogonalize; a matrix with NaN or Inf keeps
+ * lr >= 0, 0 <= beta < 1, lr and 1 - lr weight_decay within FP32.  Errors as fs4_muon_orthogonalize; a matrix with NaN or Inf keeps
  * its weights but for the decay (its momentum is updated as stated). */
 fs4_status fs4_muon_step(int32_t count, const fs4_muon_desc* descs, int32_t K,
                          const float* coeffs, int32_t n_coeffs, double lr, double beta,

@@ -1,5 +1,6 @@
 // C entry points of the Muon step (declared in include/fs4.h): argument checks, workspace plan
 // and the launch sequence.
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -129,7 +130,8 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
   if (flags & ~(uint32_t)(step ? FS4_MUON_NESTEROV : 0u)) return FS4_ERR_INVALID_ARG;
   for (int32_t i = 0; i < n_coeffs; ++i)
     if (!coeffs_ok(coeffs + 3 * i)) return FS4_ERR_INVALID_ARG;
-  if (step && (!std::isfinite(lr) || lr < 0.0 || !(beta >= 0.0 && beta < 1.0) || !std::isfinite(weight_decay)))
+  // the kernels take the rate and the decay factor in FP32, where 0 times infinity would be NaN
+  if (step && (!(lr >= 0.0 && lr <= FLT_MAX) || !(beta >= 0.0 && beta < 1.0) || !(std::fabs(1.0 - lr * weight_decay) <= FLT_MAX)))
     return FS4_ERR_INVALID_ARG;
   MuonTable& t = t_table;
   static thread_local int64_t rows[kMuonMaxBatch], cols[kMuonMaxBatch];

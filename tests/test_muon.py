@@ -123,3 +123,15 @@ def test_coefficient_ranges(F):
     for bad in ((16.5, 0, 0), (1, 256, 0), (1, 0, -256), (1, 1100, -1100), (1, float("inf"), 0), (1, 0, float("nan")),
                 (1, 3e38, -3e38), (float("-inf"), 0, 0)):
         assert call(bad) == -1 and call(steep, bad) == -1, bad
+
+
+def test_rates_outside_fp32_are_refused(F):
+    one, size = (ctypes.c_float * 3)(*O.MUON), F.muon_workspace_size([(32, 48)])
+
+    def step(lr, wd):
+        d = (F._lib.MuonDesc * 1)(_desc(F, 1 << 32))
+        return F._lib.lib().fs4_muon_step(1, d, 5, one, 1, lr, 0.9, wd, 0, 1 << 40, size - 1, None)
+
+    assert step(3e38, 0.0) == -4 and step(1e30, 1e8) == -4 and step(0.0, 1e300) == -4 and step(1e-3, -5.0) == -4
+    for lr, wd in ((1e39, 0.0), (1e30, 1e9), (1e30, -1e9), (1e300, 1e300), (float("nan"), 0.0), (0.0, float("inf"))):
+        assert step(lr, wd) == -1, (lr, wd)
