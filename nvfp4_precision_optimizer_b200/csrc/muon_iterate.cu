@@ -683,6 +683,7 @@ __device__ __forceinline__ bool finish(const MuonCall& p, Shared& sh, Deal<kPair
     if (ok && j.mat != seen && (E != kGram || it > 0)) {
       if (lane == 0) ok = wait_count(muon_counts(p.ws) + j.mat, units_before<kPair, E>(sh, j.mat, it), muon_status(p.ws), abort);
       ok = __all_sync(0xFFFFFFFFu, ok);
+      __syncwarp();      // orders the lanes' loads behind lane 0's acquire (a vote orders nothing)
       seen = j.mat;
     }
     if (kPair && !ok) return false;
