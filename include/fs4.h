@@ -346,7 +346,7 @@ size_t fs4_mxfp4_linear_workspace_size(int64_t M, int64_t K);
  * it takes a launch of its own (up to 32 rows are quantised by the product's kernel), so
  * calls whose work overlaps on the GPU need separate workspaces.  flags: FS4_MX_SCALE_CEIL,
  * FS4_MX_ACCUMULATE.  Errors as fs4_mxfp4_gemm; FS4_ERR_ALIAS also for a workspace or D that
- * overlaps x, W or the other. */
+ * overlaps x, W or the other (x and D of one pitch may lie side by side in a buffer). */
 fs4_status fs4_mxfp4_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
                             const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, void* d,
                             int32_t d_dtype, int64_t ldd, uint32_t flags, void* workspace,
@@ -549,7 +549,7 @@ size_t fs4_muon_workspace_size(int32_t count, const int64_t* rows, const int64_t
  *   Errors: FS4_ERR_SHAPE (count outside [1, FS4_MAX_BATCH], K outside [1, FS4_MAX_ITERS], a
  *   size), FS4_ERR_INVALID_ARG (null or misaligned pointers, leading dimensions, types,
  *   coefficients, scale), FS4_ERR_ALIAS (an output overlaps an input, another output or the
- *   workspace), FS4_ERR_WORKSPACE, FS4_ERR_ARCH, FS4_ERR_CUDA; FS4_ERR_NONFINITE and
+ *   workspace; matrices of one pitch side by side in a buffer do not), FS4_ERR_WORKSPACE, FS4_ERR_ARCH, FS4_ERR_CUDA; FS4_ERR_NONFINITE and
  *   FS4_ERR_TIMEOUT in the status word, which each call resets.  Calls whose work overlaps on
  *   the GPU need separate workspaces. */
 fs4_status fs4_muon_orthogonalize(int32_t count, const fs4_muon_desc* descs, int32_t K,

@@ -15,15 +15,6 @@ inline bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintpt
 inline bool known_type(int32_t t) { return t == FS4_F32 || t == FS4_BF16 || t == FS4_F16; }
 inline int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
-struct Range {
-  uintptr_t lo, hi;
-};
-inline Range range_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t type) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, lo + (uintptr_t)(((rows - 1) * ld + cols) * type_bytes(type))};
-}
-inline bool meets(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
-
 bool shape_ok(int64_t m, int64_t n) { return m >= 1 && n >= 1 && m <= FS4_MAX_DIM && n <= FS4_MAX_DIM; }
 
 int64_t parts_of(int64_t m, int64_t n) {
@@ -135,7 +126,7 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
     return FS4_ERR_INVALID_ARG;
   MuonTable& t = t_table;
   static thread_local int64_t rows[kMuonMaxBatch], cols[kMuonMaxBatch];
-  static thread_local Range out[2 * kMuonMaxBatch], in[kMuonMaxBatch];
+  static thread_local Span out[2 * kMuonMaxBatch], in[kMuonMaxBatch];
   int32_t outs = 0;
   for (int32_t i = 0; i < count; ++i) {
     const fs4_muon_desc& d = descs[i];
@@ -160,23 +151,23 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
     m.np = (int32_t)up(m.n, kMuonPad);
     rows[i] = d.rows;
     cols[i] = d.cols;
-    in[i] = range_of(d.g, d.rows, d.cols, d.ld_g, d.g_dtype);
-    out[outs++] = range_of(d.w, d.rows, d.cols, d.ld_w, d.w_dtype);
-    if (step) out[outs++] = range_of(d.m, d.rows, d.cols, d.ld_m, d.m_dtype);
+    in[i] = matrix_at(d.g, d.rows, d.cols, d.ld_g, d.g_dtype);
+    out[outs++] = matrix_at(d.w, d.rows, d.cols, d.ld_w, d.w_dtype);
+    if (step) out[outs++] = matrix_at(d.m, d.rows, d.cols, d.ld_m, d.m_dtype);
   }
   const Plan pl = plan(count, rows, cols, &t);
   const int64_t need = pl.bytes;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < (size_t)need) return FS4_ERR_WORKSPACE;
-  const Range ws{reinterpret_cast<uintptr_t>(workspace), reinterpret_cast<uintptr_t>(workspace) + (uintptr_t)need};
+  const Span ws = bytes_at(workspace, need);
   for (int32_t i = 0; i < outs; ++i) {
-    if (meets(out[i], ws)) return FS4_ERR_ALIAS;
+    if (meet(out[i], ws)) return FS4_ERR_ALIAS;
     for (int32_t k = 0; k < count; ++k)
-      if (meets(out[i], in[k])) return FS4_ERR_ALIAS;
+      if (meet(out[i], in[k])) return FS4_ERR_ALIAS;
     for (int32_t k = i + 1; k < outs; ++k)
-      if (meets(out[i], out[k])) return FS4_ERR_ALIAS;
+      if (meet(out[i], out[k])) return FS4_ERR_ALIAS;
   }
   for (int32_t k = 0; k < count; ++k)
-    if (meets(in[k], ws)) return FS4_ERR_ALIAS;
+    if (meet(in[k], ws)) return FS4_ERR_ALIAS;
   int sms = 0;
   const fs4_status ds = current_device(&sms);
   if (ds != FS4_OK) return ds;

@@ -10,21 +10,12 @@ inline fs4_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FS4_OK 
 inline bool known_type(int32_t t) { return t == FS4_F32 || t == FS4_BF16 || t == FS4_F16; }
 inline int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
-// Half-open byte ranges.
-struct Range {
-  uintptr_t lo, hi;
-  Range(const void* p, int64_t bytes) : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + (uintptr_t)(p ? bytes : 0)) {}
-  bool meets(const Range& o) const { return lo < o.hi && o.lo < hi; }
-};
-Range matrix_range(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t type) {
-  return Range(p, ((rows - 1) * ld + cols) * type_bytes(type));
-}
 // Codes and scales of a rows x K view.
-Range code_range(const void* p, int64_t rows, int64_t K, bool tiled) {
-  return Range(p, tiled ? up(rows, 128) * up(K, 256) / 2 : rows * ((K + 1) / 2));
+Span code_range(const void* p, int64_t rows, int64_t K, bool tiled) {
+  return bytes_at(p, tiled ? up(rows, 128) * up(K, 256) / 2 : rows * ((K + 1) / 2));
 }
-Range scale_range(const void* p, int64_t rows, int64_t K, bool tiled) {
-  return Range(p, tiled ? up(rows, 128) * up(K, 256) / 32 : rows * ((K + 31) / 32));
+Span scale_range(const void* p, int64_t rows, int64_t K, bool tiled) {
+  return bytes_at(p, tiled ? up(rows, 128) * up(K, 256) / 32 : rows * ((K + 31) / 32));
 }
 
 constexpr int64_t kMxMaxDim = int64_t(1) << 31;
@@ -41,9 +32,9 @@ fs4_status check_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uin
       !aligned(d, type_bytes(d_dtype)))
     return FS4_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < kMxHeader) return FS4_ERR_WORKSPACE;
-  const Range out = matrix_range(d, M, N, ldd, d_dtype), header(workspace, kMxHeader);
-  if (out.meets(code_range(a_codes, M, K, true)) || out.meets(scale_range(a_scales, M, K, true)) ||
-      out.meets(code_range(b_codes, N, K, true)) || out.meets(scale_range(b_scales, N, K, true)) || out.meets(header))
+  const Span out = matrix_at(d, M, N, ldd, d_dtype), header = bytes_at(workspace, kMxHeader);
+  if (meet(out, code_range(a_codes, M, K, true)) || meet(out, scale_range(a_scales, M, K, true)) ||
+      meet(out, code_range(b_codes, N, K, true)) || meet(out, scale_range(b_scales, N, K, true)) || meet(out, header))
     return FS4_ERR_ALIAS;
   return FS4_OK;
 }
@@ -65,12 +56,12 @@ fs4_status fs4_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_
       !aligned(col_scales, 16))
     return FS4_ERR_INVALID_ARG;
   const bool tiled = (flags & FS4_LAYOUT_TILED) != 0;
-  const Range r[5] = {matrix_range(x, rows, cols, ld, dtype), code_range(row_codes, rows, cols, tiled),
+  const Span r[5] = {matrix_at(x, rows, cols, ld, dtype), code_range(row_codes, rows, cols, tiled),
                       scale_range(row_scales, rows, cols, tiled), code_range(col_codes, cols, rows, tiled),
                       scale_range(col_scales, cols, rows, tiled)};
   for (int i = 0; i < 5; ++i)
     for (int j = i + 1; j < 5; ++j)
-      if (r[i].meets(r[j])) return FS4_ERR_ALIAS;
+      if (meet(r[i], r[j])) return FS4_ERR_ALIAS;
   int sms = 0;
   const fs4_status ds = current_device(&sms);
   if (ds != FS4_OK) return ds;
@@ -87,8 +78,8 @@ fs4_status fs4_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int
   if (ld < cols || ld > INT64_MAX / 4 / rows) return FS4_ERR_INVALID_ARG;
   if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(y, type_bytes(dtype))) return FS4_ERR_INVALID_ARG;
   const bool tiled = (flags & FS4_LAYOUT_TILED) != 0;
-  const Range out = matrix_range(y, rows, cols, ld, dtype);
-  if (out.meets(code_range(codes, rows, cols, tiled)) || out.meets(scale_range(scales, rows, cols, tiled))) return FS4_ERR_ALIAS;
+  const Span out = matrix_at(y, rows, cols, ld, dtype);
+  if (meet(out, code_range(codes, rows, cols, tiled)) || meet(out, scale_range(scales, rows, cols, tiled))) return FS4_ERR_ALIAS;
   int sms = 0;
   const fs4_status ds = current_device(&sms);
   if (ds != FS4_OK) return ds;
@@ -125,11 +116,11 @@ fs4_status fs4_mxfp4_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FS4_ERR_WORKSPACE;
   uint8_t* codes = static_cast<uint8_t*>(workspace) + kMxHeader;
   uint8_t* scales = codes + up(M, 128) * up(K, 256) / 2;
-  const Range ws(workspace, (int64_t)need), xr = matrix_range(x, M, K, ldx, x_dtype);
-  if (ws.meets(xr) || ws.meets(code_range(w_codes, N, K, true)) || ws.meets(scale_range(w_scales, N, K, true))) return FS4_ERR_ALIAS;
+  const Span ws = bytes_at(workspace, (int64_t)need), xr = matrix_at(x, M, K, ldx, x_dtype);
+  if (meet(ws, xr) || meet(ws, code_range(w_codes, N, K, true)) || meet(ws, scale_range(w_scales, N, K, true))) return FS4_ERR_ALIAS;
   if (ldd >= N && ldd <= INT64_MAX / 4 / M) {
-    const Range out = matrix_range(d, M, N, ldd, d_dtype);
-    if (out.meets(ws) || out.meets(xr)) return FS4_ERR_ALIAS;
+    const Span out = matrix_at(d, M, N, ldd, d_dtype);
+    if (meet(out, ws) || meet(out, xr)) return FS4_ERR_ALIAS;
   }
   // the product's checks come before the quantisation is enqueued
   fs4_status s = check_gemm(codes, scales, w_codes, w_scales, M, N, K, d, d_dtype, ldd, workspace, need);

@@ -13,6 +13,33 @@ namespace fs4 {
 constexpr int kTypeF32 = 0, kTypeBf16 = 1, kTypeF16 = 2;
 inline int64_t type_bytes(int dtype) { return dtype == kTypeF32 ? 4 : 2; }
 
+// The bytes of a matrix or a buffer: [lo, hi), of which rows of `width` bytes, `pitch` apart, are its
+// own (pitch 0: all of them).
+struct Span {
+  uintptr_t lo, hi;
+  uint64_t pitch, width;
+};
+inline Span bytes_at(const void* p, int64_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + (uintptr_t)(p ? bytes : 0), 0, (uint64_t)(p ? bytes : 0)};
+}
+inline Span matrix_at(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t type) {
+  Span s = bytes_at(p, ((rows - 1) * ld + cols) * type_bytes(type));
+  if (rows > 1) s.pitch = (uint64_t)(ld * type_bytes(type));
+  s.width = (uint64_t)(cols * type_bytes(type));
+  return s;
+}
+// Whether two of them share a byte.  Matrices of one pitch may lie side by side, as column slices of
+// one buffer do: modulo the pitch a's rows are [0, a.width) and b's start at d.  Different pitches
+// count as overlapping where their ranges do.
+inline bool meet(const Span& a, const Span& b) {
+  if (!(a.lo < b.hi && b.lo < a.hi)) return false;
+  const uint64_t pitch = a.pitch ? a.pitch : b.pitch;
+  if (pitch == 0 || (b.pitch != 0 && b.pitch != pitch)) return true;
+  const uint64_t d = b.lo >= a.lo ? (b.lo - a.lo) % pitch : (pitch - (a.lo - b.lo) % pitch) % pitch;
+  return !(d >= a.width && d + b.width <= pitch);
+}
+
 // The current device's SM count; FS4_ERR_ARCH off sm_100 (api.cu).
 fs4_status current_device(int* num_sms);
 

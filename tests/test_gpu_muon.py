@@ -354,3 +354,26 @@ def test_iterates_that_leave_the_operands_range_are_reported(fs4):
         ws = torch.empty(fs4.muon_workspace_size([(64, 64)]), dtype=torch.uint8, device="cuda")
         fs4.muon_orthogonalize([x], K=len(per), coeffs=per, workspace=ws)
         assert fs4.device_status(ws) == -7
+
+
+@pytest.mark.parametrize("shapes", [[(300, 40), (300, 200), (300, 7)], [(20, 33), (20, 31)], [(1300, 1024), (1300, 1400)]], ids=str)
+def test_slices_of_one_buffer_step_as_matrices_of_their_own(fs4, shapes):
+    """Projections stored side by side, gradients and momenta too, at odd offsets."""
+    rows, total = shapes[0][0], sum(n for _, n in shapes)
+    buffers = [make(rows, total + 3, t, k).cuda() for t, k in ((torch.float32, 1), (torch.bfloat16, 2), (torch.float32, 3))]
+    at = [1 + sum(n for _, n in shapes[:i]) for i in range(len(shapes))]
+    cut = lambda b: [b[:, c:c + n] for c, (_, n) in zip(at, shapes)]  # noqa: E731
+    alone = [[t.clone() for t in cut(b)] for b in buffers]
+    edges = [b[:, [0, -2, -1]].clone() for b in buffers]
+    fs4.muon_step(*map(cut, buffers), lr=0.1, weight_decay=0.1)
+    fs4.muon_step(*alone, lr=0.1, weight_decay=0.1)
+    for b, ts, e in zip(buffers, alone, edges):
+        assert torch.equal(b[:, [0, -2, -1]], e)
+        for x, y in zip(cut(b), ts):
+            # rows off 16 bytes add their squares up in another order: X_0 may differ by a step of
+            # FP32, which moves one in 2^12 of its elements by 2^-11 in the operands
+            assert far(x, np64(y)) <= 2.0 ** -15
+    assert all(torch.equal(x, y) for b, ts in zip(buffers[1:], alone[1:]) for x, y in zip(cut(b), ts))
+    with pytest.raises(fs4.Fs4Error):
+        fs4.muon_step([buffers[0][:, :9], buffers[0][:, 8:20]], [g[:, :w] for g, w in zip(cut(buffers[1])[:1] * 2, (9, 12))],
+                      [torch.zeros(rows, w, device="cuda") for w in (9, 12)], lr=0.1)

@@ -273,3 +273,19 @@ def test_refusals_on_device(fs4):
         fs4.mxfp4_linear(x, view, 8, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(fs4.Fs4Error):
         fs4.mxfp4_dequantize(view[0][:8192].view(-1), view[0][8192:], 8, 64, out=view[0].view(torch.float32)[:512].view(8, 64))
+
+
+@pytest.mark.parametrize("M", (3, 40, 600))
+def test_linear_between_slices_of_one_buffer(fs4, M):
+    """x and D side by side in one buffer."""
+    N, K = 520, 640
+    w = fs4.mxfp4_quantize(make(N, K, torch.float32, 3).cuda() / 64, tiled=True)
+    x = make(M, K, torch.bfloat16).cuda()
+    want = fs4.mxfp4_linear(x, w, N)
+    buffer = torch.full((M, 4 + K + N + 3), 5.0, dtype=torch.bfloat16, device="cuda")
+    buffer[:, 4:4 + K] = x
+    fs4.mxfp4_linear(buffer[:, 4:4 + K], w, N, out=buffer[:, 4 + K:4 + K + N])
+    assert torch.equal(buffer[:, 4 + K:4 + K + N], want) and torch.equal(buffer[:, 4:4 + K], x)
+    assert (buffer[:, :4] == 5).all() and (buffer[:, -3:] == 5).all()
+    with pytest.raises(fs4.Fs4Error):
+        fs4.mxfp4_linear(buffer[:, 4:4 + K], w, N, out=buffer[:, 3 + K:3 + K + N])

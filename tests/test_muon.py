@@ -135,3 +135,33 @@ def test_rates_outside_fp32_are_refused(F):
     assert step(3e38, 0.0) == -4 and step(1e30, 1e8) == -4 and step(0.0, 1e300) == -4 and step(1e-3, -5.0) == -4
     for lr, wd in ((1e39, 0.0), (1e30, 1e9), (1e30, -1e9), (1e300, 1e300), (float("nan"), 0.0), (0.0, float("inf"))):
         assert step(lr, wd) == -1, (lr, wd)
+
+
+def test_column_slices_overlap_where_they_share_a_byte(F):
+    """Weights, gradients and momenta of two matrices as slices of one buffer."""
+    lib, one = F._lib.lib(), (ctypes.c_float * 3)(*O.MUON)
+    need, base, ws = F.muon_workspace_size([(32, 48)] * 2), 1 << 32, 1 << 40
+
+    def step(offset, cols=(48, 48), ld=(400, 400), what="w", rows=(32, 32), space=ws):
+        """Matrix 1's `what` starts `offset` bytes after matrix 0's w."""
+        arr = (F._lib.MuonDesc * 2)(_desc(F, base), _desc(F, base + (5 << 28)))
+        for d, c, r in zip(arr, cols, rows):
+            d.cols, d.rows = c, r
+        arr[0].ld_w = ld[0]
+        setattr(arr[1], what, base + offset)
+        setattr(arr[1], "ld_" + what, ld[1])
+        setattr(arr[1], what + "_dtype", 0)
+        return lib.fs4_muon_step(2, arr, 5, one, 1, 1e-3, 0.9, 0.0, 1, space, need, None)
+
+    for what in "wgm":
+        for shared in (47 * 4, 48 * 4 - 4, 1600 - 47 * 4, 1600 * 31, 0, -47 * 4, -1600 + 47 * 4, 1600 * 3 + 4):
+            assert step(shared, what=what) == -3, (what, shared)
+        assert step(48 * 4, ld=(400, 408), what=what) == -3             # another pitch
+    assert step(360 * 4) == -3                                          # the second's rows reach the first's next ones
+    assert step(48 * 4, space=base + 512) == -3                         # a workspace over the gaps
+    if torch.cuda.is_available():
+        pytest.skip("the accepted calls would launch on these addresses")
+    for what in "wgm":
+        for apart in (48 * 4, 1600 - 48 * 4, 1600 * 31 + 48 * 4, -48 * 4, -1600 + 48 * 4, 1600 * 40):
+            assert step(apart, what=what) in (-5, -6), (what, apart)    # as far as the device check
+    assert step(48 * 4, rows=(32, 1), ld=(400, 48)) in (-5, -6)         # one row has no pitch
