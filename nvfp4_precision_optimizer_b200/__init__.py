@@ -252,6 +252,8 @@ def _mx_scale_flag(scale_rule: str) -> int:
 
 def _mx_quantize(x, row, col, tiled, scale_rule, seed):
     flags = _mx_scale_flag(scale_rule) | (FS4_LAYOUT_TILED if tiled else 0)
+    if x.numel() == 0:           # as an expert without tokens has; the views are empty too
+        return
     if seed is None:
         seed = 0
     else:
@@ -315,6 +317,13 @@ def _mx_out(out, rows: int, cols: int, dtype, device):
     return out
 
 
+def _mx_empty(d, K: int, accumulate: bool) -> bool:
+    """Whether a product has no rows, columns or terms; without terms D is 0, or stays."""
+    if K == 0 and not accumulate:
+        d.zero_()
+    return K == 0 or d.numel() == 0
+
+
 def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, tiled: bool = False,
                      dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values of a rows x cols MXFP4 matrix (fs4_mxfp4_dequantize) in `dtype`, or in `out`."""
@@ -324,6 +333,8 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols:
         with _at(dev, stream):
             return mxfp4_dequantize(codes, scales, rows, cols, tiled, dtype, out)
     y = _mx_out(out, rows, cols, dtype, dev)
+    if y.numel() == 0:
+        return y
     check(_lib.lib().fs4_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, y.data_ptr(), _DTYPES[y.dtype],
                                           _ld(y), FS4_LAYOUT_TILED if tiled else 0, _handle(dev)),
           "fs4_mxfp4_dequantize")
@@ -333,8 +344,8 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols:
 def mxfp4_gemm(a, b, M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
                accumulate: bool = False, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """D = deq(A) deq(B)^T, or D += with accumulate (fs4_mxfp4_gemm); a and b are (codes,
-    scales) in the TILED layout, A M x K and B N x K.  A workspace of the caller's is zeroed
-    once, before its first call."""
+    scales) in the TILED layout, A M x K and B N x K.  M, N or K may be 0, as for an expert
+    without tokens.  A workspace of the caller's is zeroed once, before its first call."""
     dev = a[0].device
     _mx_check(a, M, K, True, "a", dev)
     _mx_check(b, N, K, True, "b", dev)
@@ -344,6 +355,8 @@ def mxfp4_gemm(a, b, M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16
         with _at(dev, stream):
             return mxfp4_gemm(a, b, M, N, K, dtype, out, accumulate, workspace)
     d = _mx_out(out, M, N, dtype, dev)
+    if _mx_empty(d, K, accumulate):
+        return d
     if workspace is None:
         workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
     else:
@@ -374,6 +387,8 @@ def mxfp4_linear(x: torch.Tensor, w, N: int, dtype: torch.dtype | None = None, s
         with _at(dev, stream):
             return mxfp4_linear(x, w, N, dtype, scale_rule, out, accumulate, workspace)
     d = _mx_out(out, M, N, x.dtype if dtype is None else dtype, dev)
+    if _mx_empty(d, K, accumulate):
+        return d
     need = 256 + 17 * mxfp4_tiled_shape(M, K)[1]             # mxfp4_linear_workspace_size(M, K)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)

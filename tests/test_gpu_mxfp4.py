@@ -289,3 +289,44 @@ def test_linear_between_slices_of_one_buffer(fs4, M):
     assert (buffer[:, :4] == 5).all() and (buffer[:, -3:] == 5).all()
     with pytest.raises(fs4.Fs4Error):
         fs4.mxfp4_linear(buffer[:, 4:4 + K], w, N, out=buffer[:, 3 + K:3 + K + N])
+
+
+@pytest.mark.parametrize("tiled", (False, True), ids=("plain", "tiled"))
+def test_no_rows_give_empty_views(fs4, tiled):
+    for rows, cols in ((0, 96), (5, 0), (0, 0)):
+        x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+        for seed in (None, 3):
+            row, col = fs4.mxfp4_quantize_both(x, tiled=tiled, seed=seed)
+            for view, (r, c) in ((row, (rows, cols)), (col, (cols, rows)), (fs4.mxfp4_quantize(x, tiled=tiled), (rows, cols)),
+                                 (fs4.mxfp4_quantize(x, axis=fs4.FS4_AXIS_COL, tiled=tiled), (cols, rows))):
+                assert all(t.numel() == 0 and t.dtype is torch.uint8 and t.is_cuda for t in view)
+                y = fs4.mxfp4_dequantize(*view, r, c, tiled=tiled, dtype=torch.float16)
+                assert y.shape == (r, c) and y.dtype is torch.float16
+    with pytest.raises(ValueError):
+        fs4.mxfp4_quantize(torch.zeros(0, 4, device="cuda"), scale_rule="nearest")
+
+
+def test_an_expert_without_tokens_trains_like_the_others(fs4):
+    """y, dx and dW of a linear layer for token counts with a zero among them."""
+    n_in, n_out = 96, 160
+    wr, wc = fs4.mxfp4_quantize_both(make(n_out, n_in, torch.float32).cuda(), tiled=True)
+    for tokens in (0, 3):
+        x, dy = make(tokens, n_in, torch.bfloat16, 1).cuda(), make(tokens, n_out, torch.bfloat16, 2).cuda()
+        _, xc = fs4.mxfp4_quantize_both(x, tiled=True)
+        gr, gc = fs4.mxfp4_quantize_both(dy, tiled=True)
+        assert fs4.mxfp4_linear(x, wr, n_out).shape == (tokens, n_out)
+        assert fs4.mxfp4_linear(x, wr, n_out, dtype=torch.float32).dtype is torch.float32
+        assert fs4.mxfp4_gemm(gr, wc, tokens, n_in, n_out).shape == (tokens, n_in)
+        dw = torch.full((n_out, n_in), 2.0, device="cuda")
+        fs4.mxfp4_gemm(gc, xc, n_out, n_in, tokens, out=dw, accumulate=True)
+        assert (dw == 2).all() == (tokens == 0)
+        fs4.mxfp4_gemm(gc, xc, n_out, n_in, tokens, out=dw)
+        assert dw.any() == (tokens > 0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    empty = torch.zeros(0, dtype=torch.uint8, device="cuda")
+    y = fs4.mxfp4_gemm((empty, empty), (empty, empty), 7, 9, 0, stream=side)
+    side.synchronize()
+    assert y.shape == (7, 9) and not y.any()
+    with pytest.raises(ValueError):
+        fs4.mxfp4_gemm((empty, empty), (empty, empty), 7, 9, 1)
