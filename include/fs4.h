@@ -342,9 +342,8 @@ size_t fs4_mxfp4_linear_workspace_size(int64_t M, int64_t K);
 /* D = Q(x) deq(W)^T: x (M x K of `x_dtype`, leading dimension ldx) is quantised to the MXFP4
  * row view (nearest; flags may hold FS4_MX_SCALE_CEIL) and multiplied with W (N x K, TILED)
  * as by fs4_mxfp4_gemm; equal to the two calls bit for bit.  The first 256 bytes of the
- * workspace are the status word, to be zeroed once; the rest holds Q(x) where
- * it takes a launch of its own (up to 32 rows are quantised by the product's kernel), so
- * calls whose work overlaps on the GPU need separate workspaces.  flags: FS4_MX_SCALE_CEIL,
+ * workspace are the status word, to be zeroed once; any call may write Q(x) to the rest, whatever
+ * its number of rows, so calls whose work overlaps on the GPU need separate workspaces.  flags: FS4_MX_SCALE_CEIL,
  * FS4_MX_ACCUMULATE.  Errors as fs4_mxfp4_gemm; FS4_ERR_ALIAS also for a workspace or D that
  * overlaps x, W or the other (x and D of one pitch may lie side by side in a buffer). */
 fs4_status fs4_mxfp4_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,

@@ -330,3 +330,24 @@ def test_an_expert_without_tokens_trains_like_the_others(fs4):
     assert y.shape == (7, 9) and not y.any()
     with pytest.raises(ValueError):
         fs4.mxfp4_gemm((empty, empty), (empty, empty), 7, 9, 1)
+
+
+def test_linears_at_once_with_workspaces_of_their_own(fs4):
+    """Any row count may keep Q(x) in its workspace: calls on two streams, none waiting for the other."""
+    N, K = 700, 4096
+    w = fs4.mxfp4_quantize(make(N, K, torch.float32, 3).cuda() / 64, tiled=True)
+    rows = (1, 3, 16, 17, 32, 33, 200)
+    xs = [make(M, K, torch.bfloat16, s).cuda() for s in (0, 1) for M in rows]
+    want = [fs4.mxfp4_linear(x, w, N) for x in xs]
+    spaces = [torch.zeros(fs4.mxfp4_linear_workspace_size(max(rows), K), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        for i in range(len(rows)):
+            for s in range(2):
+                k = s * len(rows) + i
+                outs.append((k, fs4.mxfp4_linear(xs[k], w, N, workspace=spaces[s], stream=streams[s])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[k]) for k, o in outs)
+    assert all(fs4.device_status(ws) == 0 for ws in spaces)
