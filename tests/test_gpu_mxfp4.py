@@ -351,3 +351,25 @@ def test_linears_at_once_with_workspaces_of_their_own(fs4):
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[k]) for k, o in outs)
     assert all(fs4.device_status(ws) == 0 for ws in spaces)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("size", [(141, 1000, 700), (500, 130, 2100), (1500, 1400, 300), (1025, 1501, 2304), (2300, 2048, 96)], ids=str)
+def test_linear_of_many_rows_against_float64(fs4, size, kind):
+    """The tile and the pair kernel behind the launch that quantises their operand."""
+    M, N, K = size
+    t = TYPES[kind]
+    x = (make(M, K + 2, t) / 64).cuda()[:, 1:-1]
+    wv = make(N, K, torch.float32, 3) / 64
+    w = fs4.mxfp4_quantize(wv.cuda(), tiled=True)
+    ws = torch.zeros(fs4.mxfp4_linear_workspace_size(M, K), dtype=torch.uint8, device="cuda")
+    got = fs4.mxfp4_linear(x, w, N, workspace=ws)
+    assert torch.equal(got, fs4.mxfp4_gemm(fs4.mxfp4_quantize(x, tiled=True), w, M, N, K, dtype=t))
+    a, b = O.values(*O.quantize(np64(x))), O.values(*O.quantize(np64(wv)))
+    want, bound = a @ b.T, K * 2.0 ** -23 * (np.abs(a) @ np.abs(b).T)
+    tiny = float(torch.finfo(t).smallest_normal) * float(torch.finfo(t).eps)
+    assert (np.abs(np64(got) - want) <= bound + HALF_STEP[t] * (np.abs(want) + bound) + tiny).all()
+    d = torch.full((M, N), 1.0, device="cuda")
+    fs4.mxfp4_linear(x, w, N, out=d, accumulate=True, workspace=ws)
+    assert (np.abs(np64(d) - want - 1) <= bound + 2.0 ** -23 * (np.abs(want) + bound + 1)).all()
+    assert fs4.device_status(ws) == 0
