@@ -351,6 +351,14 @@ fs4_status fs4_mxfp4_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K
                             int32_t d_dtype, int64_t ldd, uint32_t flags, void* workspace,
                             size_t workspace_bytes, void* stream);
 
+/* As fs4_mxfp4_linear, with the status word in the first of the 256 bytes at `status` (256-byte
+ * aligned) instead of the workspace's, which need not be zeroed then: several calls, each with a
+ * workspace of its own, can report to one word. */
+fs4_status fs4_mxfp4_linear_ex(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
+                               const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, void* d,
+                               int32_t d_dtype, int64_t ldd, uint32_t flags, void* workspace,
+                               size_t workspace_bytes, void* status, void* stream);
+
 /* ----------------------------------------------------------- Newton-Schulz */
 
 /* One matrix of a batched call.  G (input) and out (output) are m x n FP32

@@ -213,6 +213,21 @@ def _at(device: torch.device, stream):
         yield
 
 
+# Where MXFP4 and Muon calls without a workspace of the caller's report: 256 bytes for each stream,
+# zero at first and after device_status() has read them.
+_status_words: dict[tuple[int, int], torch.Tensor] = {}
+
+
+def _status_word(device: torch.device) -> torch.Tensor:
+    key = (device.index, _handle(device))
+    word = _status_words.get(key)
+    if word is None:
+        word = torch.zeros(256, dtype=torch.uint8, device=device)
+        if not torch.cuda.is_current_stream_capturing():     # (a graph's memory is not ours to keep)
+            word = _status_words.setdefault(key, word)
+    return word
+
+
 def mxfp4_tiled_shape(rows: int, cols: int) -> tuple[int, int]:
     """(codes bytes, scales bytes) of a rows x cols MXFP4 matrix in the TILED layout."""
     padded = (rows + 127) // 128 * 128 * ((cols + 255) // 256 * 256)
@@ -358,7 +373,7 @@ def mxfp4_gemm(a, b, M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16
     if _mx_empty(d, K, accumulate):
         return d
     if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+        workspace = _status_word(dev)
     else:
         _check_bytes(workspace, 256, "workspace", dev)
     check(_lib.lib().fs4_mxfp4_gemm(a[0].data_ptr(), a[1].data_ptr(), b[0].data_ptr(), b[1].data_ptr(), M, N, K, d.data_ptr(),
@@ -391,14 +406,14 @@ def mxfp4_linear(x: torch.Tensor, w, N: int, dtype: torch.dtype | None = None, s
         return d
     need = 256 + 17 * mxfp4_tiled_shape(M, K)[1]             # mxfp4_linear_workspace_size(M, K)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        workspace[:256].zero_()
+        workspace, status = torch.empty(need, dtype=torch.uint8, device=dev), _status_word(dev)
     else:
         _check_bytes(workspace, need, "workspace", dev)
-    check(_lib.lib().fs4_mxfp4_linear(x.data_ptr(), _DTYPES[x.dtype], M, K, _ld(x), w[0].data_ptr(), w[1].data_ptr(), N,
-                                      d.data_ptr(), _DTYPES[d.dtype], _ld(d),
-                                      _mx_scale_flag(scale_rule) | (_lib.FS4_MX_ACCUMULATE if accumulate else 0),
-                                      workspace.data_ptr(), workspace.numel(), _handle(dev)),
+        status = workspace
+    check(_lib.lib().fs4_mxfp4_linear_ex(x.data_ptr(), _DTYPES[x.dtype], M, K, _ld(x), w[0].data_ptr(), w[1].data_ptr(), N,
+                                         d.data_ptr(), _DTYPES[d.dtype], _ld(d),
+                                         _mx_scale_flag(scale_rule) | (_lib.FS4_MX_ACCUMULATE if accumulate else 0),
+                                         workspace.data_ptr(), workspace.numel(), status.data_ptr(), _handle(dev)),
           "fs4_mxfp4_linear")
     return d
 
@@ -428,7 +443,8 @@ def _muon_call(ws_list, gs, ms, scales, K, coeffs, workspace, step):
         if m is not None:
             d.m, d.ld_m, d.m_dtype = m.data_ptr(), _ld(m), _DTYPES[m.dtype]
     c, nc = _muon_coeffs(coeffs, K)
-    if workspace is None:
+    own = workspace is None
+    if own:
         workspace = torch.empty(max(muon_workspace_size([g.shape for g in gs]), 1), dtype=torch.uint8, device=dev)
     else:      # the call itself checks its size
         _check_bytes(workspace, 1, "workspace", dev)
@@ -438,6 +454,8 @@ def _muon_call(ws_list, gs, ms, scales, K, coeffs, workspace, step):
     else:
         check(_lib.lib().fs4_muon_step(n, arr, K, c, nc, *step, workspace.data_ptr(), workspace.numel(), _handle(dev)),
               "fs4_muon_step")
+    if own:       # each call resets the word in its workspace
+        _status_word(dev)[:4].view(torch.int32).bitwise_or_(workspace[:4].view(torch.int32))
 
 
 def muon_orthogonalize(Gs: Sequence[torch.Tensor], K: int = 5, coeffs=MUON_COEFFS, dtype: torch.dtype = torch.bfloat16,
@@ -685,9 +703,24 @@ def ns_layout(shapes: Sequence[tuple[int, int]], index: int = 0) -> NsLayout:
     return lay
 
 
-def device_status(workspace: torch.Tensor, stream=None) -> int:
-    """Synchronise and return the device status word of the last call (0 = FS4_OK)."""
-    return int(_lib.lib().fs4_device_status(workspace.data_ptr(), _stream(stream)))
+def device_status(workspace: torch.Tensor | None = None, stream=None) -> int:
+    """Synchronise and return the device status word of the last call (0 = FS4_OK).  Without a
+    workspace: that of all mxfp4_* and muon_* calls since the last such query, on any stream of
+    any device, that were not given one (calls captured into a graph should be: their status is
+    kept only where their stream has made such a call outside the capture)."""
+    if workspace is not None:
+        return int(_lib.lib().fs4_device_status(workspace.data_ptr(), _stream(stream)))
+    worst = 0
+    for device in {word.device for word in list(_status_words.values())}:
+        with torch.cuda.device(device):
+            torch.cuda.synchronize()
+            for word in [w for w in list(_status_words.values()) if w.device == device]:
+                status = int(_lib.lib().fs4_device_status(word.data_ptr(), None))
+                if status != 0:
+                    word.zero_()
+                worst = min(worst, status)
+            torch.cuda.synchronize()
+    return worst
 
 
 GEMM_SOURCES = ("gemm.cu", "fs4_device.cuh", "fs4_internal.h")

@@ -86,6 +86,8 @@ SIGNATURES = {
     "fs4_mxfp4_linear_workspace_size": (c_sz, [c_i64, c_i64]),
     "fs4_mxfp4_linear": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp, c_i32, c_i64,
                                  c_u32, c_vp, c_sz, c_vp]),
+    "fs4_mxfp4_linear_ex": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp, c_i32, c_i64,
+                                    c_u32, c_vp, c_sz, c_vp, c_vp]),
     "fs4_muon_workspace_size": (c_sz, [c_i32, ctypes.POINTER(c_i64), ctypes.POINTER(c_i64)]),
     "fs4_muon_orthogonalize": (c_i32, [c_i32, ctypes.POINTER(MuonDesc), c_i32, ctypes.POINTER(c_f32), c_i32, c_vp,
                                        c_sz, c_vp]),

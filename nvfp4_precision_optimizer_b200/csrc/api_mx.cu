@@ -108,12 +108,20 @@ size_t fs4_mxfp4_linear_workspace_size(int64_t M, int64_t K) {
 fs4_status fs4_mxfp4_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t* w_codes,
                             const uint8_t* w_scales, int64_t N, void* d, int32_t d_dtype, int64_t ldd, uint32_t flags,
                             void* workspace, size_t workspace_bytes, void* stream) {
+  return fs4_mxfp4_linear_ex(x, x_dtype, M, K, ldx, w_codes, w_scales, N, d, d_dtype, ldd, flags, workspace, workspace_bytes, workspace,
+                             stream);
+}
+
+fs4_status fs4_mxfp4_linear_ex(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t* w_codes,
+                               const uint8_t* w_scales, int64_t N, void* d, int32_t d_dtype, int64_t ldd, uint32_t flags,
+                               void* workspace, size_t workspace_bytes, void* status, void* stream) {
   if (!x || !w_codes || !w_scales || !d || !known_type(x_dtype) || !known_type(d_dtype)) return FS4_ERR_INVALID_ARG;
   if (flags & ~(uint32_t)(FS4_MX_SCALE_CEIL | FS4_MX_ACCUMULATE)) return FS4_ERR_INVALID_ARG;
   if (M < 1 || N < 1 || K < 1 || M > kMxMaxGemm || N > kMxMaxGemm || K > kMxMaxGemm) return FS4_ERR_SHAPE;
   if (ldx < K || ldx > INT64_MAX / 4 / M) return FS4_ERR_INVALID_ARG;
   const size_t need = fs4_mxfp4_linear_workspace_size(M, K);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FS4_ERR_WORKSPACE;
+  if (!status || !aligned(status, 256)) return FS4_ERR_WORKSPACE;
   uint8_t* codes = static_cast<uint8_t*>(workspace) + kMxHeader;
   uint8_t* scales = codes + up(M, 128) * up(K, 256) / 2;
   const Span ws = bytes_at(workspace, (int64_t)need), xr = matrix_at(x, M, K, ldx, x_dtype);
@@ -122,21 +130,26 @@ fs4_status fs4_mxfp4_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K
     const Span out = matrix_at(d, M, N, ldd, d_dtype);
     if (meet(out, ws) || meet(out, xr)) return FS4_ERR_ALIAS;
   }
+  if (status != workspace) {
+    const Span word = bytes_at(status, kMxHeader);
+    if (meet(word, ws) || meet(word, xr) || meet(word, code_range(w_codes, N, K, true)) || meet(word, scale_range(w_scales, N, K, true)))
+      return FS4_ERR_ALIAS;
+  }
   // the product's checks come before the quantisation is enqueued
-  fs4_status s = check_gemm(codes, scales, w_codes, w_scales, M, N, K, d, d_dtype, ldd, workspace, need);
+  fs4_status s = check_gemm(codes, scales, w_codes, w_scales, M, N, K, d, d_dtype, ldd, status, kMxHeader);
   if (s != FS4_OK) return s;
   if (!aligned(x, type_bytes(x_dtype))) return FS4_ERR_INVALID_ARG;
   int sms = 0;
   if ((s = current_device(&sms)) != FS4_OK) return s;
   MxLinearArgs l{x, w_codes, w_scales, M, N, K, ldx, d, ldd, x_dtype, d_dtype, (flags & FS4_MX_ACCUMULATE) ? 1 : 0,
-                 (flags & FS4_MX_SCALE_CEIL) ? 1 : 0, static_cast<uint32_t*>(workspace)};
+                 (flags & FS4_MX_SCALE_CEIL) ? 1 : 0, static_cast<uint32_t*>(status)};
   cudaError_t e = cudaSuccess;
   if (mxfp4_linear_fused(l, static_cast<cudaStream_t>(stream), sms, &e)) return cuda_status(e);
   s = fs4_mxfp4_quantize(x, x_dtype, M, K, ldx, codes, scales, nullptr, nullptr, FS4_LAYOUT_TILED | (flags & FS4_MX_SCALE_CEIL), 0,
                          stream);
   if (s != FS4_OK) return s;
   MxGemmArgs g{codes, scales, w_codes, w_scales, M, N, K, d, ldd, d_dtype, (flags & FS4_MX_ACCUMULATE) ? 1 : 0,
-               static_cast<uint32_t*>(workspace), 1};
+               static_cast<uint32_t*>(status), 1};
   return cuda_status(launch_mxfp4_gemm(g, static_cast<cudaStream_t>(stream), sms));
 }
 

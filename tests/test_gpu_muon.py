@@ -377,3 +377,52 @@ def test_slices_of_one_buffer_step_as_matrices_of_their_own(fs4, shapes):
     with pytest.raises(fs4.Fs4Error):
         fs4.muon_step([buffers[0][:, :9], buffers[0][:, 8:20]], [g[:, :w] for g, w in zip(cut(buffers[1])[:1] * 2, (9, 12))],
                       [torch.zeros(rows, w, device="cuda") for w in (9, 12)], lr=0.1)
+
+
+def test_status_of_calls_without_a_workspace(fs4):
+    fs4.device_status()                           # what earlier calls left
+    good, bad = make(40, 70).cuda(), make(300, 200).cuda()
+    bad[299, 3] = float("nan")
+    fs4.muon_orthogonalize([good])
+    assert fs4.device_status() == 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        fs4.muon_orthogonalize([bad, good], stream=stream)
+        fs4.muon_orthogonalize([good], stream=stream)              # does not hide it
+        assert fs4.device_status() == -7 and fs4.device_status() == 0
+        fs4.muon_step([torch.zeros_like(bad)], [bad], [torch.zeros_like(bad)], lr=0.1, stream=stream)
+        assert fs4.device_status() == -7 and fs4.device_status() == 0
+    ws = torch.empty(fs4.muon_workspace_size([bad.shape]), dtype=torch.uint8, device="cuda")
+    fs4.muon_orthogonalize([bad], workspace=ws)
+    assert fs4.device_status(ws) == -7 and fs4.device_status() == 0
+
+
+def test_calls_without_a_workspace_in_graphs(fs4):
+    """Captured on a stream that made no such call before, and on one that did."""
+    G = make(64, 100).cuda()
+    w = fs4.mxfp4_quantize(make(64, 100).cuda(), tiled=True)
+    want, y = fs4.muon_orthogonalize([G])[0], fs4.mxfp4_linear(G, w, 64)
+    p = fs4.mxfp4_gemm(w, w, 64, 64, 100)
+    fs4.device_status()
+    for warm in (False, True):
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        if warm:
+            fs4.mxfp4_gemm(w, w, 64, 64, 100, stream=stream)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            outs = [fs4.muon_orthogonalize([G])[0], fs4.mxfp4_linear(G, w, 64), fs4.mxfp4_gemm(w, w, 64, 64, 100)]
+        for _ in range(2):
+            for o in outs:
+                o.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs, (want, y, p)))
+        assert fs4.device_status() == 0
+        if warm:
+            kept = G.clone()
+            G[3, 3] = float("inf")
+            graph.replay()
+            assert fs4.device_status() == -7
+            G.copy_(kept)

@@ -129,3 +129,21 @@ def test_tiled_sizes(F):
     assert F.mxfp4_tiled_shape(129, 257) == (256 * 256, 256 * 16)
     c, s = O.pack_tiled(*O.quantize(np.ones((129, 257))))
     assert (len(c), len(s)) == F.mxfp4_tiled_shape(129, 257)
+
+
+def test_linear_with_a_status_word_of_its_own_refusals(F):
+    lib, p = F._lib.lib(), 1 << 20
+    far = [p * 4 ** i for i in range(1, 8)]
+    need = lib.fs4_mxfp4_linear_workspace_size(5, 7)
+    good = [far[0], 1, 5, 7, 7, far[1], far[2], 6, far[3], 1, 6, 0, far[4], need, far[5], None]
+
+    def linear(**kw):
+        a = list(good)
+        for k, v in kw.items():
+            a[int(k[1:])] = v
+        return lib.fs4_mxfp4_linear_ex(*a)
+
+    assert linear(_14=None) == -4 and linear(_14=far[5] + 128) == -4 and linear(_13=need - 1) == -4
+    assert linear(_14=far[4] + 256) == -3 and linear(_14=far[0]) == -3 and linear(_14=far[1]) == -3
+    assert linear(_14=far[2]) == -3 and linear(_14=far[3]) == -3 and linear(_8=far[4] + 512) == -3
+    assert F.device_status() == 0                       # no call was made, and no device is needed
