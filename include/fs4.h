@@ -117,9 +117,11 @@ enum {
  * before the preamble writes X_0 there. */
 #define FS4_NS_CLIP_QUANTILE (1u << 4)
 
-/* Test-only flag for fs4_root_ns / fs4_root_ns_batched and fs4_nvfp4_quantize
- * (no counterpart in the paper).  Newton-Schulz: the MMA issuer of the first
- * Gram product waits on a barrier that nothing arrives on.  Quantise: the grid
+/* Test-only flag for fs4_root_ns / fs4_root_ns_batched, fs4_nvfp4_quantize, fs4_mxfp4_gemm,
+ * fs4_mxfp4_linear and fs4_muon_step (no counterpart in the paper).
+ * Newton-Schulz: the MMA issuer of the first Gram product waits on a barrier
+ * that nothing arrives on; MXFP4 products and Muon (matrices of more than 32
+ * rows and columns): every MMA issuer does.  Quantise: the grid
  * barrier between the amax pass and the quantise pass waits for one CTA more
  * than the launch has.  The bounded wait gives up after about 2 s, records the
  * timeout in the status word, and the rest of the call's work is skipped;

@@ -357,10 +357,11 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols:
 
 
 def mxfp4_gemm(a, b, M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
-               accumulate: bool = False, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+               accumulate: bool = False, workspace: torch.Tensor | None = None, stream=None, flags: int = 0) -> torch.Tensor:
     """D = deq(A) deq(B)^T, or D += with accumulate (fs4_mxfp4_gemm); a and b are (codes,
     scales) in the TILED layout, A M x K and B N x K.  M, N or K may be 0, as for an expert
-    without tokens.  A workspace of the caller's is zeroed once, before its first call."""
+    without tokens.  A workspace of the caller's is zeroed once, before its first call.
+    flags: extra call flags (FS4_TEST_STALL for the timeout test)."""
     dev = a[0].device
     _mx_check(a, M, K, True, "a", dev)
     _mx_check(b, N, K, True, "b", dev)
@@ -368,7 +369,7 @@ def mxfp4_gemm(a, b, M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16
         raise ValueError("accumulate needs out")
     if not _here(dev, stream):
         with _at(dev, stream):
-            return mxfp4_gemm(a, b, M, N, K, dtype, out, accumulate, workspace)
+            return mxfp4_gemm(a, b, M, N, K, dtype, out, accumulate, workspace, None, flags)
     d = _mx_out(out, M, N, dtype, dev)
     if _mx_empty(d, K, accumulate):
         return d
@@ -377,7 +378,7 @@ def mxfp4_gemm(a, b, M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16
     else:
         _check_bytes(workspace, 256, "workspace", dev)
     check(_lib.lib().fs4_mxfp4_gemm(a[0].data_ptr(), a[1].data_ptr(), b[0].data_ptr(), b[1].data_ptr(), M, N, K, d.data_ptr(),
-                                    _DTYPES[d.dtype], _ld(d), _lib.FS4_MX_ACCUMULATE if accumulate else 0,
+                                    _DTYPES[d.dtype], _ld(d), flags | (_lib.FS4_MX_ACCUMULATE if accumulate else 0),
                                     workspace.data_ptr(), workspace.numel(), _handle(dev)),
           "fs4_mxfp4_gemm")
     return d
@@ -389,9 +390,10 @@ def mxfp4_linear_workspace_size(M: int, K: int) -> int:
 
 def mxfp4_linear(x: torch.Tensor, w, N: int, dtype: torch.dtype | None = None, scale_rule: str = "floor",
                  out: torch.Tensor | None = None, accumulate: bool = False, workspace: torch.Tensor | None = None,
-                 stream=None) -> torch.Tensor:
+                 stream=None, flags: int = 0) -> torch.Tensor:
     """Q(x) deq(W)^T for an FP32, BF16 or FP16 x (M x K) and TILED MXFP4 weights w = (codes,
-    scales), N x K (fs4_mxfp4_linear); in x's type unless dtype or out says otherwise."""
+    scales), N x K (fs4_mxfp4_linear); in x's type unless dtype or out says otherwise.
+    flags as mxfp4_gemm."""
     _check_matrix(x, "x")
     M, K = x.shape
     dev = x.device
@@ -400,7 +402,7 @@ def mxfp4_linear(x: torch.Tensor, w, N: int, dtype: torch.dtype | None = None, s
         raise ValueError("accumulate needs out")
     if not _here(dev, stream):
         with _at(dev, stream):
-            return mxfp4_linear(x, w, N, dtype, scale_rule, out, accumulate, workspace)
+            return mxfp4_linear(x, w, N, dtype, scale_rule, out, accumulate, workspace, None, flags)
     d = _mx_out(out, M, N, x.dtype if dtype is None else dtype, dev)
     if _mx_empty(d, K, accumulate):
         return d
@@ -412,7 +414,7 @@ def mxfp4_linear(x: torch.Tensor, w, N: int, dtype: torch.dtype | None = None, s
         status = workspace
     check(_lib.lib().fs4_mxfp4_linear_ex(x.data_ptr(), _DTYPES[x.dtype], M, K, _ld(x), w[0].data_ptr(), w[1].data_ptr(), N,
                                          d.data_ptr(), _DTYPES[d.dtype], _ld(d),
-                                         _mx_scale_flag(scale_rule) | (_lib.FS4_MX_ACCUMULATE if accumulate else 0),
+                                         flags | _mx_scale_flag(scale_rule) | (_lib.FS4_MX_ACCUMULATE if accumulate else 0),
                                          workspace.data_ptr(), workspace.numel(), status.data_ptr(), _handle(dev)),
           "fs4_mxfp4_linear")
     return d
@@ -489,11 +491,11 @@ def _muon_scale(scale, rows: int, cols: int) -> float:
 
 def muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], momenta: Sequence[torch.Tensor], lr: float,
               beta: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0, K: int = 5, coeffs=MUON_COEFFS,
-              scale="rms", workspace: torch.Tensor | None = None, stream=None) -> None:
+              scale="rms", workspace: torch.Tensor | None = None, stream=None, flags: int = 0) -> None:
     """One Muon step on every matrix, in place (fs4_muon_step): momentum, orthogonalised
     direction, decoupled weight decay, weights.  Each tensor is FP32, BF16 or FP16.  scale:
     "rms" multiplies the direction by 0.2 sqrt(max(rows, cols)), "spectral" by
-    sqrt(max(1, rows / cols)); or a number."""
+    sqrt(max(1, rows / cols)); or a number.  flags as mxfp4_gemm."""
     if not (len(params) == len(grads) == len(momenta)):
         raise ValueError("params, grads and momenta must be lists of one length")
     if not params:
@@ -506,9 +508,10 @@ def muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], mom
                 raise ValueError(f"{name}[{i}] must have the shape of params[{i}], {tuple(ts[0].shape)}")
     if not _here(dev, stream):
         with _at(dev, stream):
-            return muon_step(params, grads, momenta, lr, beta, nesterov, weight_decay, K, coeffs, scale, workspace)
+            return muon_step(params, grads, momenta, lr, beta, nesterov, weight_decay, K, coeffs, scale, workspace,
+                             None, flags)
     _muon_call(params, grads, momenta, [_muon_scale(scale, *p.shape) for p in params], K, coeffs, workspace,
-               (lr, beta, weight_decay, _lib.FS4_MUON_NESTEROV if nesterov else 0))
+               (lr, beta, weight_decay, flags | (_lib.FS4_MUON_NESTEROV if nesterov else 0)))
 
 
 def _ld(t: torch.Tensor) -> int:

@@ -118,7 +118,7 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
   if (!descs || !coeffs) return FS4_ERR_INVALID_ARG;
   if (count < 1 || count > kMuonMaxBatch || K < 1 || K > FS4_MAX_ITERS) return FS4_ERR_SHAPE;
   if (n_coeffs != 1 && n_coeffs != K) return FS4_ERR_INVALID_ARG;
-  if (flags & ~(uint32_t)(step ? FS4_MUON_NESTEROV : 0u)) return FS4_ERR_INVALID_ARG;
+  if (flags & ~(uint32_t)(step ? FS4_MUON_NESTEROV | FS4_TEST_STALL : 0u)) return FS4_ERR_INVALID_ARG;
   for (int32_t i = 0; i < n_coeffs; ++i)
     if (!coeffs_ok(coeffs + 3 * i)) return FS4_ERR_INVALID_ARG;
   // the kernels take the rate and the decay factor in FP32, where 0 times infinity would be NaN
@@ -197,6 +197,7 @@ fs4_status run(int32_t count, const fs4_muon_desc* descs, bool step, int32_t K, 
   c.parts_at = pl.parts_at;
   c.counts_at = pl.counts_at;
   c.counts = (int32_t)pl.counts;
+  c.stall = (flags & FS4_TEST_STALL) ? 1 : 0;
   std::memcpy(c.coeffs, coeffs, sizeof(float) * 3 * n_coeffs);
   if (launch_muon_moment(c, t, st) != cudaSuccess) return FS4_ERR_CUDA;
   if (t.prefix[kUnitsThin][count] && launch_muon_thin(c, t.prefix[kUnitsThin][count], st) != cudaSuccess) return FS4_ERR_CUDA;

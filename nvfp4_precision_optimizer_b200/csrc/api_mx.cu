@@ -89,14 +89,14 @@ fs4_status fs4_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int
 fs4_status fs4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes, const uint8_t* b_scales,
                           int64_t M, int64_t N, int64_t K, void* d, int32_t d_dtype, int64_t ldd, uint32_t flags, void* workspace,
                           size_t workspace_bytes, void* stream) {
-  if (flags & ~(uint32_t)FS4_MX_ACCUMULATE) return FS4_ERR_INVALID_ARG;
+  if (flags & ~(uint32_t)(FS4_MX_ACCUMULATE | FS4_TEST_STALL)) return FS4_ERR_INVALID_ARG;
   const fs4_status s = check_gemm(a_codes, a_scales, b_codes, b_scales, M, N, K, d, d_dtype, ldd, workspace, workspace_bytes);
   if (s != FS4_OK) return s;
   int sms = 0;
   const fs4_status ds = current_device(&sms);
   if (ds != FS4_OK) return ds;
   MxGemmArgs g{a_codes, a_scales, b_codes, b_scales, M, N, K, d, ldd, d_dtype, (flags & FS4_MX_ACCUMULATE) ? 1 : 0,
-               static_cast<uint32_t*>(workspace), 0};
+               static_cast<uint32_t*>(workspace), 0, (flags & FS4_TEST_STALL) ? 1 : 0};
   return cuda_status(launch_mxfp4_gemm(g, static_cast<cudaStream_t>(stream), sms));
 }
 
@@ -116,7 +116,7 @@ fs4_status fs4_mxfp4_linear_ex(const void* x, int32_t x_dtype, int64_t M, int64_
                                const uint8_t* w_scales, int64_t N, void* d, int32_t d_dtype, int64_t ldd, uint32_t flags,
                                void* workspace, size_t workspace_bytes, void* status, void* stream) {
   if (!x || !w_codes || !w_scales || !d || !known_type(x_dtype) || !known_type(d_dtype)) return FS4_ERR_INVALID_ARG;
-  if (flags & ~(uint32_t)(FS4_MX_SCALE_CEIL | FS4_MX_ACCUMULATE)) return FS4_ERR_INVALID_ARG;
+  if (flags & ~(uint32_t)(FS4_MX_SCALE_CEIL | FS4_MX_ACCUMULATE | FS4_TEST_STALL)) return FS4_ERR_INVALID_ARG;
   if (M < 1 || N < 1 || K < 1 || M > kMxMaxGemm || N > kMxMaxGemm || K > kMxMaxGemm) return FS4_ERR_SHAPE;
   if (ldx < K || ldx > INT64_MAX / 4 / M) return FS4_ERR_INVALID_ARG;
   const size_t need = fs4_mxfp4_linear_workspace_size(M, K);
@@ -142,14 +142,14 @@ fs4_status fs4_mxfp4_linear_ex(const void* x, int32_t x_dtype, int64_t M, int64_
   int sms = 0;
   if ((s = current_device(&sms)) != FS4_OK) return s;
   MxLinearArgs l{x, w_codes, w_scales, M, N, K, ldx, d, ldd, x_dtype, d_dtype, (flags & FS4_MX_ACCUMULATE) ? 1 : 0,
-                 (flags & FS4_MX_SCALE_CEIL) ? 1 : 0, static_cast<uint32_t*>(status)};
+                 (flags & FS4_MX_SCALE_CEIL) ? 1 : 0, static_cast<uint32_t*>(status), (flags & FS4_TEST_STALL) ? 1 : 0};
   cudaError_t e = cudaSuccess;
   if (mxfp4_linear_fused(l, static_cast<cudaStream_t>(stream), sms, &e)) return cuda_status(e);
   s = fs4_mxfp4_quantize(x, x_dtype, M, K, ldx, codes, scales, nullptr, nullptr, FS4_LAYOUT_TILED | (flags & FS4_MX_SCALE_CEIL), 0,
                          stream);
   if (s != FS4_OK) return s;
   MxGemmArgs g{codes, scales, w_codes, w_scales, M, N, K, d, ldd, d_dtype, (flags & FS4_MX_ACCUMULATE) ? 1 : 0,
-               static_cast<uint32_t*>(status), 1};
+               static_cast<uint32_t*>(status), 1, l.stall};
   return cuda_status(launch_mxfp4_gemm(g, static_cast<cudaStream_t>(stream), sms));
 }
 

@@ -62,6 +62,7 @@ struct MuonCall {
   int32_t split_steps;     // small: 64-element K steps of one part of a split Gram product
   int64_t parts_at, counts_at;   // small: partial tiles and their counts, bytes into the workspace
   int32_t counts;
+  int32_t stall;           // test only: the MMA issuers wait on a barrier nothing arrives on
   float coeffs[3 * FS4_MAX_ITERS];
 };
 

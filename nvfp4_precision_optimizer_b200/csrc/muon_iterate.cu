@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
       Ring<kPair> ring;
       Deal<kPair> deal;
       uint32_t tl = 0;
-      bool ok = true;
+      bool ok = !p.stall || mbar_wait(&sh.done, 0, status, abort);     // (test only: a wait that runs out)
       for (int ph = 0; ph < 3 * p.K && ok; ++ph) {
         const int e = ph % 3;
         ok = e == kGram ? multiply<kPair, kGram>(p, sh, ring, deal, tl, base, tmem, abort)

@@ -63,6 +63,7 @@ struct MxGemmArgs {
   int32_t accumulate;
   uint32_t* status;
   int32_t after_quantize;   // the launch before quantises A: overlap its end
+  int32_t stall;            // test only: the MMA issuer waits on a barrier nothing arrives on
 };
 cudaError_t launch_mxfp4_pair(const MxGemmArgs& a, cudaStream_t st);   // mxfp4_pair.cu
 // A few rows of x times W in one launch that quantises x on its way; false where x does not fit.
@@ -76,6 +77,7 @@ struct MxLinearArgs {
   int32_t x_dtype, d_dtype;
   int32_t accumulate, ceil_rule;
   uint32_t* status;
+  int32_t stall;
 };
 bool mxfp4_linear_fused(const MxLinearArgs& a, cudaStream_t st, int num_sms, cudaError_t* error);
 cudaError_t launch_mxfp4_gemm(const MxGemmArgs& a, cudaStream_t st, int num_sms);

@@ -38,6 +38,7 @@ struct TileArgs {
   int64_t ldx;
   int32_t x_dtype, K;
   int32_t ceil_rule;
+  int32_t stall;       // see MxGemmArgs
   int32_t vec;         // x's rows start on 16-byte boundaries
 };
 
@@ -284,10 +285,12 @@ __global__ void __launch_bounds__(kTileThreads) mxfp4_tile_kernel(const __grid_c
     uint64_t dq = sdesc_sw128(kFused ? smem_addr(q_all) : base + C::kP + 2 * C::kSf);
     uint64_t dqs = sdesc_sf_atom(kFused ? smem_addr(q_all) + C::kQ : base + C::kP + C::kSf);
     const uint64_t dq0 = dq, dqs0 = dqs;
-    if (kFused) mbar_wait(ready, 0, a.status, abort_flag);
+    // test only: a wait that runs out
+    bool ok = !a.stall || mbar_wait(done, 0, a.status, abort_flag);
+    if (kFused && ok) ok = mbar_wait(ready, 0, a.status, abort_flag);
     // Q rows from q0 on start at this 32-row group of their scale atom
     const uint32_t qcol = TN < 32 ? 0u : (uint32_t)((q0 & 127) >> 5);   // (a 16-row tile is the only one)
-    for (int k = k0; k < k1; ++k) {
+    for (int k = k0; ok && k < k1; ++k) {
       if (!mbar_wait(&full[s], ph, a.status, abort_flag)) break;
       tc_fence_after();
       // each stage has scale columns of its own: P's two atoms, then Q's two
@@ -429,6 +432,7 @@ cudaError_t launch_mxfp4_gemm(const MxGemmArgs& g, cudaStream_t st, int num_sms)
   a.kt = (int32_t)((g.K + 255) / 256);
   a.d = g.d; a.dtype = g.dtype; a.accumulate = g.accumulate; a.status = g.status;
   a.after_quantize = g.after_quantize;
+  a.stall = g.stall;
   const int tn = a.Q <= 16 ? 16 : a.Q <= 32 ? 32 : a.Q <= 64 ? 64 : 128;
   a.q_tiles = (a.Q + tn - 1) / tn;
   const int64_t tiles = (int64_t)((a.P + 127) / 128) * a.q_tiles;
@@ -453,6 +457,7 @@ bool mxfp4_linear_fused(const MxLinearArgs& g, cudaStream_t st, int num_sms, cud
   a.kt = (int32_t)((g.K + 255) / 256);
   a.d = g.d; a.dtype = g.d_dtype; a.accumulate = g.accumulate; a.status = g.status;
   a.x = g.x; a.ldx = g.ldx; a.x_dtype = g.x_dtype; a.K = (int32_t)g.K; a.ceil_rule = g.ceil_rule;
+  a.stall = g.stall;
   a.vec = reinterpret_cast<uintptr_t>(g.x) % 16 == 0 && (g.M == 1 || g.ldx * type_bytes(g.x_dtype) % 16 == 0);
   a.q_tiles = 1;
   const int64_t tiles = (g.N + 127) / 128;

@@ -53,6 +53,7 @@ struct PairArgs {
   int32_t accumulate;
   int32_t after_quantize;
   uint32_t* status;
+  int32_t stall;              // see MxGemmArgs
 };
 
 __device__ __forceinline__ void tile_of(const PairArgs& a, int32_t u, int32_t& I, int32_t& J) {
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_pair_kernel(const __grid_co
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     uint32_t s = 0, ph = 0, tl = 0;
-    bool ok = true;
+    bool ok = !a.stall || mbar_wait(&sh.done[0], 0, a.status, abort);     // (test only: a wait that runs out)
     const uint64_t da0 = sdesc_sw128(base), db0 = sdesc_sw128(base + kCodes);
     constexpr uint64_t kStep = kStage >> 4;
     for (int32_t u = first; u < total && ok; u += step, ++tl) {
@@ -306,6 +307,7 @@ cudaError_t launch_mxfp4_pair(const MxGemmArgs& g, cudaStream_t st) {
   a.accumulate = g.accumulate;
   a.after_quantize = g.after_quantize;
   a.status = g.status;
+  a.stall = g.stall;
   switch (g.dtype) {
     case kTypeF32: return launch_pair<float>(a, st);
     case kTypeBf16: return launch_pair<__nv_bfloat16>(a, st);

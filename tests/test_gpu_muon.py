@@ -426,3 +426,22 @@ def test_calls_without_a_workspace_in_graphs(fs4):
             graph.replay()
             assert fs4.device_status() == -7
             G.copy_(kept)
+
+
+@pytest.mark.parametrize("shapes", [[(64, 200)], [(64, 4096), (20, 30), (200, 300)], [(1500, 1900)], [(20, 700), (600, 2100), (1300, 900)]], ids=str)
+def test_wait_that_runs_out_is_reported(fs4, shapes):
+    """FS4_TEST_STALL on both kernels, with Gram products split along K and thin matrices among the
+    others: the call ends, the status word tells, and the next call in the workspace is right."""
+    import time
+    ws = torch.zeros(fs4.muon_workspace_size(shapes), dtype=torch.uint8, device="cuda")
+    G = [make(*s, torch.bfloat16).cuda() for s in shapes]
+    W, M, W2, M2 = ([torch.zeros(s, device="cuda") for s in shapes] for _ in range(4))
+    t0 = time.time()
+    fs4.muon_step([torch.zeros_like(w) for w in W], G, [torch.zeros_like(m) for m in M], lr=0.1, workspace=ws,
+                  flags=fs4.FS4_TEST_STALL)
+    assert fs4.device_status(ws) == -8
+    assert time.time() - t0 < 60.0
+    fs4.muon_step(W, G, M, lr=0.1, workspace=ws)
+    assert fs4.device_status(ws) == 0
+    fs4.muon_step(W2, G, M2, lr=0.1)
+    assert all(torch.equal(a, b) for a, b in zip(W + M, W2 + M2))

@@ -373,3 +373,40 @@ def test_linear_of_many_rows_against_float64(fs4, size, kind):
     fs4.mxfp4_linear(x, w, N, out=d, accumulate=True, workspace=ws)
     assert (np.abs(np64(d) - want - 1) <= bound + 2.0 ** -23 * (np.abs(want) + bound + 1)).all()
     assert fs4.device_status(ws) == 0
+
+
+@pytest.mark.parametrize("size", [(40, 130, 300), (64, 256, 4096), (140, 150, 300), (1300, 1500, 512)], ids=str)
+def test_gemm_wait_that_runs_out_is_reported(fs4, size):
+    """FS4_TEST_STALL: the MMA issuers wait on a barrier nothing arrives on, give up and the call
+    ends; the next one is right."""
+    import time
+    M, N, K = size
+    (a, _), (b, _) = operand(fs4, M, K, 1), operand(fs4, N, K, 2)
+    want = fs4.mxfp4_gemm(a, b, M, N, K)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    fs4.device_status()
+    t0 = time.time()
+    for space in (ws, None):
+        fs4.mxfp4_gemm(a, b, M, N, K, workspace=space, flags=fs4.FS4_TEST_STALL)
+        assert fs4.device_status(space) == -8
+    assert time.time() - t0 < 60.0
+    ws.zero_()
+    assert torch.equal(fs4.mxfp4_gemm(a, b, M, N, K, workspace=ws), want)
+    assert torch.equal(fs4.mxfp4_gemm(a, b, M, N, K), want)
+    assert fs4.device_status(ws) == 0 and fs4.device_status() == 0
+
+
+@pytest.mark.parametrize("size", [(1, 200, 512), (40, 200, 512), (1500, 1300, 300)], ids=str)
+def test_linear_wait_that_runs_out_is_reported(fs4, size):
+    M, N, K = size
+    x = make(M, K, torch.bfloat16).cuda()
+    w = fs4.mxfp4_quantize(make(N, K, torch.float32, 3).cuda() / 64, tiled=True)
+    want = fs4.mxfp4_linear(x, w, N)
+    ws = torch.zeros(fs4.mxfp4_linear_workspace_size(M, K), dtype=torch.uint8, device="cuda")
+    fs4.device_status()
+    for space in (ws, None):
+        fs4.mxfp4_linear(x, w, N, workspace=space, flags=fs4.FS4_TEST_STALL)
+        assert fs4.device_status(space) == -8
+    ws.zero_()
+    assert torch.equal(fs4.mxfp4_linear(x, w, N, workspace=ws), want) and torch.equal(fs4.mxfp4_linear(x, w, N), want)
+    assert fs4.device_status(ws) == 0 and fs4.device_status() == 0

@@ -165,3 +165,10 @@ def test_column_slices_overlap_where_they_share_a_byte(F):
         for apart in (48 * 4, 1600 - 48 * 4, 1600 * 31 + 48 * 4, -48 * 4, -1600 + 48 * 4, 1600 * 40):
             assert step(apart, what=what) in (-5, -6), (what, apart)    # as far as the device check
     assert step(48 * 4, rows=(32, 1), ld=(400, 48)) in (-5, -6)         # one row has no pitch
+
+
+def test_stall_flag_of_the_step(F):
+    one, size = (ctypes.c_float * 3)(*O.MUON), F.muon_workspace_size([(32, 48)])
+    d = (F._lib.MuonDesc * 1)(_desc(F, 1 << 32))
+    step = lambda flags: F._lib.lib().fs4_muon_step(1, d, 5, one, 1, 0.1, 0.9, 0.0, flags, 1 << 40, size - 1, None)  # noqa: E731
+    assert step(F.FS4_TEST_STALL) == -4 and step(F.FS4_TEST_STALL | 1) == -4 and step(F.FS4_TEST_STALL | 2) == -1

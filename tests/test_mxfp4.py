@@ -147,3 +147,15 @@ def test_linear_with_a_status_word_of_its_own_refusals(F):
     assert linear(_14=far[4] + 256) == -3 and linear(_14=far[0]) == -3 and linear(_14=far[1]) == -3
     assert linear(_14=far[2]) == -3 and linear(_14=far[3]) == -3 and linear(_8=far[4] + 512) == -3
     assert F.device_status() == 0                       # no call was made, and no device is needed
+
+
+def test_stall_flag_is_the_products_alone(F):
+    lib, p = F._lib.lib(), 1 << 20
+    far = [p * 4 ** i for i in range(1, 7)]
+    stall = F.FS4_TEST_STALL
+    assert lib.fs4_mxfp4_quantize(far[0], 1, 5, 7, 7, far[1], far[2], None, None, stall, 0, None) == -1
+    assert lib.fs4_mxfp4_dequantize(far[0], far[1], 4, 8, far[2], 0, 8, stall, None) == -1
+    gemm = lambda flags: lib.fs4_mxfp4_gemm(*far[:4], 5, 6, 7, far[4], 0, 6, flags, None, 256, None)  # noqa: E731
+    assert gemm(stall) == -4 and gemm(stall | 128) == -4 and gemm(stall | 1) == -1
+    linear = lambda flags: lib.fs4_mxfp4_linear(far[0], 1, 5, 7, 7, far[1], far[2], 6, far[3], 1, 6, flags, None, 0, None)  # noqa: E731
+    assert linear(stall) == -4 and linear(stall | 32 | 128) == -4 and linear(stall | 2) == -1
