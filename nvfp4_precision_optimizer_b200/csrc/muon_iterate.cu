@@ -80,6 +80,7 @@ struct Shared {
   uint64_t done;
   uint32_t tmem;
   int32_t abort;
+  uint32_t issued[2];          // (leader) stages that each CTA's producer issued
   int32_t arrived;             // CTAs that had finished their part of a split product
   alignas(16) float diag[8][128];   // an epilogue warp's columns of A's diagonal
   int32_t prefix[3][kMuonMaxBatch + 1];   // units of the three products
@@ -781,13 +782,9 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
              : e == kSquare ? produce<kPair, kSquare>(p, maps, sh, ring, deal, it, base, rank, abort)
                             : produce<kPair, kUpdate>(p, maps, sh, ring, deal, it, base, rank, abort);
       }
-      // every copy lands before the pair may exit (they count on the leader's barriers)
-      if (rank == 0) {
-        for (uint32_t i = ring.issued > (uint32_t)T::kStages ? ring.issued - T::kStages : 0u; i < ring.issued; ++i) {
-          volatile int never = 0;
-          mbar_wait(&sh.full[i % T::kStages], (i / T::kStages) & 1u, status, &never);
-        }
-      }
+      // every copy lands before the CTA or the pair may exit (a pair's count on the leader's barriers)
+      if (rank == 0) await_own(sh.full, T::kStages, ring.issued, status);
+      if constexpr (kPair) tell_issued(&sh.issued[rank], ring.issued);
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -828,6 +825,9 @@ __global__ void __launch_bounds__(kThreads, 1) muon_iterate_kernel(const __grid_
     cluster_wait();
   }
   tc_fence_after();
+  if constexpr (kPair) {
+    if (rank == 0 && threadIdx.x == 0) await_issued(sh.full, T::kStages, T::kStage, sh.issued[0], sh.issued[1], status);
+  }
   if (warp == 1) {
     if constexpr (kPair) tmem_dealloc_pair(tmem, T::kCols);
     else tmem_dealloc(tmem, T::kCols);

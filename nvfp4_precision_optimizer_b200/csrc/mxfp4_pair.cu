@@ -39,6 +39,7 @@ struct Shared {
   uint64_t done[2];
   uint32_t tmem;
   int32_t abort;
+  uint32_t issued[2];         // leader: stages that each CTA's producer issued
 };
 constexpr int kSmem = 1024 + kStages * kStage + (int)sizeof(Shared);
 static_assert(kSmem <= 232448, "over the per-CTA shared-memory limit");
@@ -166,12 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_pair_kernel(const __grid_co
       }
     }
     // every copy lands before the pair may exit (they count on the leader's barriers)
-    if (rank == 0) {
-      for (uint32_t i = issued > (uint32_t)kStages ? issued - kStages : 0u; i < issued; ++i) {
-        volatile int never = 0;
-        mbar_wait(&sh.full[i % kStages], (i / kStages) & 1u, a.status, &never);
-      }
-    }
+    if (rank == 0) await_own(sh.full, kStages, issued, a.status);
+    tell_issued(&sh.issued[rank], issued);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     uint32_t s = 0, ph = 0, tl = 0;
     bool ok = !a.stall || mbar_wait(&sh.done[0], 0, a.status, abort);     // (test only: a wait that runs out)
@@ -258,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_pair_kernel(const __grid_co
   cluster_arrive();
   cluster_wait();
   tc_fence_after();
+  if (rank == 0 && threadIdx.x == 0) await_issued(sh.full, kStages, kStage, sh.issued[0], sh.issued[1], a.status);
   if (warp == 1) tmem_dealloc_pair(tmem, kCols);
   __syncthreads();
   cluster_arrive();

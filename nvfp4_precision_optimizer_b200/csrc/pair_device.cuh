@@ -41,6 +41,29 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// A producer that gives up (a wait of its ran out) may have issued fewer or more stages than the
+// other CTA's.  The leader's barriers count the copies of both, so each says how far it got:
+// CTA 1 tells the leader before they meet, and the leader expects and awaits what CTA 1 issued
+// alone, before either may leave.  `stage` is the bytes of one CTA's part of a stage.
+__device__ __forceinline__ void tell_issued(uint32_t* slot, uint32_t issued) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(smem_addr(slot), 0)), "r"(issued) : "memory");
+}
+__device__ __forceinline__ void await_issued(uint64_t* full, uint32_t stages, uint32_t stage, uint32_t own, uint32_t other, uint32_t* status) {
+  for (uint32_t i = own; i < other; ++i) {
+    volatile int never = 0;
+    mbar_arrive_expect_tx(&full[i % stages], stage);
+    if (!mbar_wait_cluster(&full[i % stages], (i / stages) & 1u, status, &never)) break;
+  }
+}
+// The leader's own stages, before that.  A stage that CTA 1 did not issue never completes: its wait
+// runs out, and the copies of later stages had that time to land.
+__device__ __forceinline__ void await_own(uint64_t* full, uint32_t stages, uint32_t issued, uint32_t* status) {
+  for (uint32_t i = issued > stages ? issued - stages : 0u; i < issued; ++i) {
+    volatile int never = 0;
+    if (!mbar_wait(&full[i % stages], (i / stages) & 1u, status, &never)) break;
+  }
+}
+
 // Copy of `rows` (the map's box) 128-byte rows from row `row` on to this CTA's shared memory; the
 // bytes are counted on `bar`, a cluster address in either CTA of the pair.  x is always 0.
 __device__ __forceinline__ void tma_rows_pair(uint32_t dst, const CUtensorMap* map, int32_t row, uint32_t bar) {
