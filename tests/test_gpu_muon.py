@@ -445,3 +445,82 @@ def test_wait_that_runs_out_is_reported(fs4, shapes):
     assert fs4.device_status(ws) == 0
     fs4.muon_step(W2, G, M2, lr=0.1)
     assert all(torch.equal(a, b) for a, b in zip(W + M, W2 + M2))
+
+
+def takes_pairs(fs4, shapes):
+    """Whether a call runs on CTA pairs: a small call's workspace also holds partial tiles of 32 KB."""
+    up = lambda v: (v + 255) // 256 * 256  # noqa: E731
+    blocks = sum(6 * up(m) * up(n) + 6 * up(min(m, n)) ** 2 for m, n in shapes if min(m, n) > 32)
+    return fs4.muon_workspace_size(shapes) - blocks < 1 << 18
+
+
+def exact64(G, K=5, coeffs=O.MUON):
+    """oracle.muon.orthogonalize on the GPU."""
+    x = G.cuda().double()
+    tall = x.shape[0] > x.shape[1]
+    x = (x.T if tall else x) / (x.norm() + 1e-7)
+    for k in range(K):
+        a, b, c = coeffs[k] if hasattr(coeffs[0], "__len__") else coeffs
+        g = x @ x.T
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return np64(x.T if tall else x)
+
+
+LARGE = [(1500, 1900), (1900, 1501), (770, 9000), (2100, 2300), (4200, 2305)]      # 3 to 10 blocks of 256 rows
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_pairs_against_float64(fs4, shape, kind):
+    assert takes_pairs(fs4, [shape]) and not takes_pairs(fs4, [(300, 1111)])
+    G = make(*shape, TYPES[kind]).cuda()
+    want = exact64(G)
+    ws = torch.empty(fs4.muon_workspace_size([shape]), dtype=torch.uint8, device="cuda")
+    for t in TYPES.values():
+        wide = torch.full((shape[0], shape[1] + 9), 3.0, dtype=t, device="cuda")
+        out = wide[:, 4:-5] if t is TYPES[kind] else torch.empty(shape, dtype=t, device="cuda")
+        fs4.muon_orthogonalize([G], outs=[out], workspace=ws)
+        assert far(out, want) <= NEAR + half_step(t) and fs4.device_status(ws) == 0
+        assert (wide[:, :4] == 3).all() and (wide[:, -5:] == 3).all()
+
+
+@pytest.mark.parametrize("shape", [(1500, 1900), (2305, 2100)], ids=str)
+def test_pairs_products_one_iteration_at_a_time(fs4, shape):
+    assert takes_pairs(fs4, [shape])
+    G = make(*shape)
+    top = float(torch.linalg.matrix_norm(G.cuda().double(), 2) / G.double().norm())
+    for coeffs in ((1.0, 0.0, 0.0), (0.0, 1.0, 0.0), (0.0, 0.0, 1.0), (0.5, -2.0, 1.0)):
+        got = fs4.muon_orthogonalize([G.cuda()], K=1, coeffs=coeffs, dtype=torch.float32)[0]
+        want = exact64(G, 1, coeffs)
+        # as in test_products_one_iteration_at_a_time, and an absolute part: the operands hold 2^8 A and
+        # 2^8 B in FP16, whose subnormal numbers (here most of A^2) are off by up to 2^-25.  With
+        # |dA|, |dB| <= 2^-33 an element, ||dB X|| <= m 2^-33 s for the largest singular value s of X,
+        # and a change of A by dA moves A^2 X by at most 2 s^2 m 2^-33 s, b A X by |b| m 2^-33 s
+        small = min(shape) * 2.0 ** -33 * top * (1 + abs(coeffs[1]) + 2 * abs(coeffs[2]) * top ** 2) / np.linalg.norm(want)
+        assert far(got, want) <= (2.0 ** -20 if coeffs[1:] == (0.0, 0.0) else 5 * 2.0 ** -12 + small), coeffs
+    per = [O.MUON, (1.5, -0.5, 0.0), (1.875, -1.25, 0.375)]
+    assert far(fs4.muon_orthogonalize([G.cuda()], K=3, coeffs=per, dtype=torch.float32)[0], exact64(G, 3, per)) <= NEAR
+
+
+@pytest.mark.parametrize("nesterov", (False, True))
+@pytest.mark.parametrize("types", [("f32", "bf16", "f32"), ("bf16", "f32", "f16")], ids=str)
+def test_pairs_step_against_float64(fs4, types, nesterov):
+    """Several matrices of three and more blocks, thin and small ones among them: the direction
+    itself (from zero weights) and the whole step."""
+    tw, tg, tm = (TYPES[t] for t in types)
+    shapes = [(800, 1100), (20, 300), (1300, 900), (33, 64), (2100, 2200)]
+    assert takes_pairs(fs4, shapes)
+    lr, beta, wd = 0.02, 0.9, 0.1
+    for start in (0.0, 2.0):
+        W, G, M = ([make(*s, t, k).mul(f).cuda() for s in shapes] for t, k, f in ((tw, 1, start), (tg, 2, 1.0), (tm, 3, 0.5)))
+        W0, G0, M0 = ([np64(t) for t in ts] for ts in (W, G, M))
+        fs4.muon_step(W, G, M, lr=lr, beta=beta, nesterov=nesterov, weight_decay=wd)
+        for w, m, w0, g0, m0 in zip(W, M, W0, G0, M0):
+            # the bounds of test_step_against_float64
+            new, size = beta * m0 + (1 - beta) * g0, beta * np.abs(m0) + (1 - beta) * np.abs(g0)
+            tiny = float(torch.finfo(tm).smallest_normal) * float(torch.finfo(tm).eps)
+            assert (np.abs(np64(m) - new) <= 4 * 2.0 ** -24 * size + half_step(tm) * (np.abs(new) + 4 * 2.0 ** -24 * size) + tiny).all()
+            kept = np64(m)
+            step = lr * 0.2 * max(w0.shape) ** 0.5 * exact64(torch.from_numpy(beta * kept + (1 - beta) * g0 if nesterov else kept))
+            want = (1 - lr * wd) * w0 - step
+            assert np.linalg.norm(np64(w) - want) <= (NEAR + 2.0 ** -22) * np.linalg.norm(step) + (half_step(tw) + 2.0 ** -22) * np.linalg.norm(want)
