@@ -525,7 +525,9 @@ fs4_status fs4_root_ns_bf16_batched_timed(int32_t count, const fs4_ns_desc* desc
  * Frobenius) from the exact iteration, also where a few directions dominate and the rest is
  * 1e-5 of them.  It is up to 1.2e-2 where the elements of one dominant direction are all equal
  * (equal elements round alike, where others average out), and about 3e-3 for K = 10, since the
- * Muon iteration does not converge.  The result repeats bit for bit.  A zero matrix gives zero.  A
+ * Muon iteration does not converge.  The same call repeats bit for bit; a matrix's bits may differ
+ * with the other matrices of its call, whose sizes decide together on which kernel it runs and in how
+ * many parts its Gram product is summed.  A zero matrix gives zero.  A
  * matrix with NaN or Inf in U is carried as zeros (its update is zero) and recorded as
  * FS4_ERR_NONFINITE in the status word; so is a result that is not finite, as coefficients
  * that make the iteration diverge give. */
