@@ -16,6 +16,7 @@
 
 #include "fs4_device.cuh"
 #include "fs4_internal.h"
+#include "mx_device.cuh"
 
 namespace fs4 {
 namespace {
@@ -33,14 +34,10 @@ __device__ __forceinline__ float mo_block_max(float v, float* red) {
   return v;
 }
 
-// SplitMix64 (Steele, Lea and Flood, OOPSLA 2014) at counter value i of a generator
-// started at `seed`; u = its top 24 bits times 2^-24 (exact in FP32).
+// The top 24 bits of SplitMix64 at counter value i of a generator started at `seed`,
+// times 2^-24 (exact in FP32).
 __device__ __forceinline__ float splitmix_u24(uint64_t seed, uint64_t i) {
-  uint64_t z = seed + (i + 1ull) * 0x9E3779B97F4A7C15ull;
-  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
-  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
-  z ^= z >> 31;
-  return (float)(uint32_t)(z >> 40) * (1.0f / 16777216.0f);
+  return (float)(uint32_t)(splitmix64(seed, i) >> 40) * (1.0f / 16777216.0f);
 }
 
 // Stochastic E2M1 rounding of v >= 0: the magnitude code lo or lo + 1 around v, up when

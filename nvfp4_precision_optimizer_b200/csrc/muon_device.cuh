@@ -2,8 +2,6 @@
 // direction, and the owner of a work unit.
 #pragma once
 
-#include <cuda_fp16.h>
-
 #include "muon_internal.h"
 #include "mx_device.cuh"
 
@@ -18,14 +16,6 @@ __device__ __forceinline__ int owner_of(const int32_t* prefix, int count, int32_
   return lo;
 }
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float get1(const void* p, int64_t i, int type) {
-  if (type == kTypeF32) return static_cast<const float*>(p)[i];
-  if (type == kTypeBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
-}
 // Round to the type and back: what a later read sees.
 __device__ __forceinline__ float put1(void* p, int64_t i, int type, float v) {
   if (type == kTypeF32) {

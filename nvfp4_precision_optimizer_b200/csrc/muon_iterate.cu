@@ -284,7 +284,7 @@ __device__ __forceinline__ bool write_result(const MuonCall& p, const MuonMat& d
         T* e = reinterpret_cast<T*>(r[b].w);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-        put_as(e + i, result(y[(q + b) * kPer + i], blend ? get_as(e + i) : 0.0f));
+        put_as(e + i, result(y[(q + b) * kPer + i], blend ? to_f32(e[i]) : 0.0f));
         }
         store_pair(at + (q + b) * kPer, r[b]);
       }
@@ -303,7 +303,7 @@ __device__ __forceinline__ bool write_result(const MuonCall& p, const MuonMat& d
   for (int h = 0; h < 32; h += 8) {
     float old[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) old[i] = (blend && h + i < count) ? get_as(at + (h + i) * d.ldw) : 0.0f;
+    for (int i = 0; i < 8; ++i) old[i] = (blend && h + i < count) ? to_f32(at[(h + i) * d.ldw]) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (h + i < count) put_as(at + (h + i) * d.ldw, result(y[h + i], old[i]));

@@ -2,6 +2,9 @@
 // placement and the random stream.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
 #include "fs4_device.cuh"
 
 namespace fs4 {
@@ -32,6 +35,14 @@ __device__ __forceinline__ uint64_t splitmix64(uint64_t seed, uint64_t i) {
   z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
   return z ^ (z >> 31);
 }
+
+// ------------------------------------------------------------------ element types
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ void put_as(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put_as(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put_as(__half* p, float v) { *p = __float2half_rn(v); }
 
 // ------------------------------------------------------------------ tensor core, kind::mxf4
 // Instruction descriptor: E2M1 x E2M1, UE8M0 scales, K-major A and B, FP32 accumulate, M x N,

@@ -136,13 +136,6 @@ __device__ __forceinline__ void quantize_q(const TileArgs& a, uint8_t* q, int k0
   asm volatile("fence.proxy.async;" ::: "memory");     // the tensor core reads what was stored
 }
 
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-__device__ __forceinline__ void store_rounded(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_rounded(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void store_rounded(__half* p, float v) { *p = __float2half_rn(v); }
-
 // Sum the cluster's partial tiles (rank order, so the result does not depend on timing) and
 // write rows [lo, hi) of the tile's kC columns at D[r0.., c0..]: four columns a thread and load.
 template <int kC, typename T>
@@ -174,12 +167,12 @@ __device__ __forceinline__ void tile_store(const TileArgs& a, const float* part,
       struct alignas(4 * sizeof(T)) Four { T t[4]; } o;
       if (a.accumulate) o = *reinterpret_cast<const Four*>(at);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) store_rounded(&o.t[k], a.accumulate ? e[k] + to_float(o.t[k]) : e[k]);
+      for (int k = 0; k < 4; ++k) put_as(&o.t[k], a.accumulate ? e[k] + to_f32(o.t[k]) : e[k]);
       *reinterpret_cast<Four*>(at) = o;
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (c + k < cols) store_rounded(at + k, a.accumulate ? e[k] + to_float(at[k]) : e[k]);
+        if (c + k < cols) put_as(at + k, a.accumulate ? e[k] + to_f32(at[k]) : e[k]);
     }
   }
 }
@@ -232,7 +225,7 @@ __global__ void __launch_bounds__(kTileThreads) mxfp4_tile_kernel(const __grid_c
     const int64_t band = (int64_t)a.kt * kTileBytes, sband = (int64_t)a.kt * C::kSf;
     const uint8_t* pc = a.p_codes + (p0 >> 7) * band + (int64_t)k0 * kTileBytes;
     const uint8_t* ps = a.p_scales + (p0 >> 7) * sband + (int64_t)k0 * C::kSf;
-    const uint8_t* qc = a.q_codes + (q0 >> 7) * band + (int64_t)k0 * kTileBytes + (q0 & 127) * 128;
+    const uint8_t* qc = a.q_codes + (q0 >> 7) * band + (int64_t)k0 * kTileBytes;
     const uint8_t* qs = a.q_scales + (q0 >> 7) * sband + (int64_t)k0 * C::kSf;
     uint32_t s = 0, ph = 0;
     int k = k0;
@@ -288,8 +281,6 @@ __global__ void __launch_bounds__(kTileThreads) mxfp4_tile_kernel(const __grid_c
     // test only: a wait that runs out
     bool ok = !a.stall || mbar_wait(done, 0, a.status, abort_flag);
     if (kFused && ok) ok = mbar_wait(ready, 0, a.status, abort_flag);
-    // Q rows from q0 on start at this 32-row group of their scale atom
-    const uint32_t qcol = TN < 32 ? 0u : (uint32_t)((q0 & 127) >> 5);   // (a 16-row tile is the only one)
     for (int k = k0; ok && k < k1; ++k) {
       if (!mbar_wait(&full[s], ph, a.status, abort_flag)) break;
       tc_fence_after();
@@ -308,7 +299,7 @@ __global__ void __launch_bounds__(kTileThreads) mxfp4_tile_kernel(const __grid_c
 #pragma unroll
       for (int h = 0; h < 4; ++h)
         tc_mma_mxf4(tmem, dp + 2 * h, dq + 2 * h, idesc_mxf4(128, TN, h & 1), sf + 4 * (h >> 1),
-                    sf + 8 + 4 * (h >> 1) + qcol, (k > k0 || h > 0) ? 1u : 0u);
+                    sf + 8 + 4 * (h >> 1), (k > k0 || h > 0) ? 1u : 0u);
       tc_commit(&empty[s]);
       if constexpr (kFused) {
         dq += C::kQAll >> 4;
@@ -433,6 +424,7 @@ cudaError_t launch_mxfp4_gemm(const MxGemmArgs& g, cudaStream_t st, int num_sms)
   a.d = g.d; a.dtype = g.dtype; a.accumulate = g.accumulate; a.status = g.status;
   a.after_quantize = g.after_quantize;
   a.stall = g.stall;
+  // (tiles of fewer than 128 rows of Q are alone, so every tile starts a 128-row band)
   const int tn = a.Q <= 16 ? 16 : a.Q <= 32 ? 32 : a.Q <= 64 ? 64 : 128;
   a.q_tiles = (a.Q + tn - 1) / tn;
   const int64_t tiles = (int64_t)((a.P + 127) / 128) * a.q_tiles;

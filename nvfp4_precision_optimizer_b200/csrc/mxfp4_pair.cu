@@ -85,7 +85,7 @@ __device__ __forceinline__ void store_row(const PairArgs& a, int32_t row, int32_
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
         const float v = __uint_as_float(acc[(q + b) * kPer + i]);
-        put_as(e + i, a.accumulate ? v + get_as(e + i) : v);
+        put_as(e + i, a.accumulate ? v + to_f32(e[i]) : v);
         }
         store_pair(at + (q + b) * kPer, r[b]);
       }
@@ -102,7 +102,7 @@ __device__ __forceinline__ void store_row(const PairArgs& a, int32_t row, int32_
   for (int h = 0; h < 32; h += 8) {
     float old[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) old[i] = (a.accumulate && r0 + h + i < a.M) ? get_as(at + (h + i) * a.ldd) : 0.0f;
+    for (int i = 0; i < 8; ++i) old[i] = (a.accumulate && r0 + h + i < a.M) ? to_f32(at[(h + i) * a.ldd]) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (r0 + h + i < a.M) put_as(at + (h + i) * a.ldd, __uint_as_float(acc[h + i]) + old[i]);

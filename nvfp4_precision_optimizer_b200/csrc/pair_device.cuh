@@ -173,11 +173,4 @@ __device__ __forceinline__ void turn32(uint32_t* v, int lane) {
   }
 }
 
-__device__ __forceinline__ float get_as(const float* p) { return *p; }
-__device__ __forceinline__ float get_as(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float get_as(const __half* p) { return __half2float(*p); }
-__device__ __forceinline__ void put_as(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put_as(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put_as(__half* p, float v) { *p = __float2half_rn(v); }
-
 }  // namespace fs4
