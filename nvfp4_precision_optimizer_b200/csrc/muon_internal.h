@@ -114,7 +114,7 @@ __host__ __device__ inline MuonLayout muon_layout(int64_t mp, int64_t np) {
   return L;
 }
 
-// A thin matrix's block: T (m x m FP32), what U is multiplied by first (FP32, 0 if the norm is not
+// A thin matrix's block: T (m x m FP32), the factor of the products T U (FP32, 0 if the norm is not
 // finite), then one m x m FP64 Gram matrix per chunk of columns.
 __host__ __device__ inline int64_t thin_flag_offset(int64_t m) { return 4 * m * m; }
 __host__ __device__ inline int64_t thin_gram_offset(int64_t m) { return (4 * m * m + 4 + 255) / 256 * 256; }

@@ -150,12 +150,12 @@ __global__ void __launch_bounds__(1024) muon_thin_iterate_kernel(const __grid_co
     }
     __syncthreads();
   }
-  // T holds 1 / ||U||: beside a norm near FP32's largest values U is taken times 2^-64 and T times
-  // 2^64, which keeps T a normal number
-  const double shift = inv < 0x1p-100 ? 0x1p-64 : 1.0;
-  if (mine) reinterpret_cast<float*>(ws)[threadIdx.x] = fine ? (float)(T[i][j] / shift) : 0.0f;
+  // T holds 1 / ||U||: beside a norm near FP32's largest values it is stored times 2^64, which keeps
+  // it a normal number, and the products T U are taken times 2^-64
+  const bool large = inv < 0x1p-100;
+  if (mine) reinterpret_cast<float*>(ws)[threadIdx.x] = fine ? (float)(large ? T[i][j] * 0x1p64 : T[i][j]) : 0.0f;
   if (threadIdx.x == 0) {
-    *reinterpret_cast<float*>(ws + thin_flag_offset(m)) = fine ? (float)shift : 0.0f;
+    *reinterpret_cast<float*>(ws + thin_flag_offset(m)) = !fine ? 0.0f : large ? 0x1p-64f : 1.0f;
     if (!fine) atomicOr(muon_status(p.ws), kStatusNonFinite);
   }
 }
@@ -180,8 +180,6 @@ __global__ void __launch_bounds__(kThreads) muon_thin_apply_kernel(const __grid_
   for (int r = 0; r < kMuonThin; r += 8) {
     if (r < m) {
       direction_column8(p, d, r, c, u + r);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[r + i] *= shift;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[r + i] = 0.0f;
@@ -210,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) muon_thin_apply_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i0 + i >= m) break;
-      const float v = fine ? s[i] * d.scale : 0.0f;
+      const float v = fine ? s[i] * shift * d.scale : 0.0f;
       bad |= !isfinite(v);
       const int64_t at = d.tall ? c * d.ldw + i0 + i : (int64_t)(i0 + i) * d.ldw + c;
       put1(d.w, at, d.tw, blend ? fmaf(-p.rate, v, p.keep * w[i]) : v);
