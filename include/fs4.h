@@ -316,7 +316,8 @@ fs4_status fs4_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_
 
 /* The values of a rows x cols MXFP4 matrix (PLAIN, or TILED with FS4_LAYOUT_TILED) in y
  * (`dtype`, leading dimension ld), each rounded once.  BF16 and FP32 hold every value
- * exactly.  One launch.  Errors as fs4_mxfp4_quantize. */
+ * under 2^128 exactly (an element of 1.75 2^127 or more may round up to 2^128 under the ceil rule,
+ * which reads back as Inf).  One launch.  Errors as fs4_mxfp4_quantize. */
 fs4_status fs4_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
                                 int64_t cols, void* y, int32_t dtype, int64_t ld, uint32_t flags,
                                 void* stream);

@@ -410,3 +410,15 @@ def test_linear_wait_that_runs_out_is_reported(fs4, size):
     ws.zero_()
     assert torch.equal(fs4.mxfp4_linear(x, w, N, workspace=ws), want) and torch.equal(fs4.mxfp4_linear(x, w, N), want)
     assert fs4.device_status(ws) == 0 and fs4.device_status() == 0
+
+
+def test_elements_next_to_the_largest_fp32_value(fs4):
+    """The ceil rule's scale is 2^126 there: 1.75 2^127 is the tie between the codes 3 and 4, and 4 is 2^128."""
+    x = torch.zeros(1, 32, device="cuda")
+    for top, floor, ceil in ((1.5, 1.5, 1.5), (1.74, 1.5, 1.5), (1.75, 1.5, float("inf")), (1.99, 1.5, float("inf"))):
+        x[0, 0] = top * 2.0 ** 127
+        for rule, want in (("floor", floor), ("ceil", ceil)):
+            view = fs4.mxfp4_quantize(x, scale_rule=rule)
+            same(view, O.quantize(np64(x), rule), False)
+            y = fs4.mxfp4_dequantize(*view, 1, 32)
+            assert y[0, 0].item() == want * 2.0 ** 127 and not y[0, 1:].any(), (top, rule)
