@@ -522,7 +522,9 @@ fs4_status fs4_root_ns_bf16_batched_timed(int32_t count, const fs4_ns_desc* desc
  *   X_0 = U / (||U||_F + 1e-7) (transposed when rows > cols), then K times
  *   A = X X^T, B = b A + c A^2, X <- a X + B X,
  * with FP16 tensor-core operands, FP32 accumulation and FP32 diagonals of A and B kept out
- * of the operands.  With the Muon coefficients and K = 5 the result is 0.1-1.8e-3 (relative,
+ * of the operands.  X is kept to 22 significand bits or to 2^-37, whichever is more (an update whose
+ * norm is far below the 1e-7 beside it has a result near zero, right to that).  With the Muon
+ * coefficients and K = 5 the result is 0.1-1.8e-3 (relative,
  * Frobenius) from the exact iteration, also where a few directions dominate and the rest is
  * 1e-5 of them.  It is up to 1.2e-2 where the elements of one dominant direction are all equal
  * (equal elements round alike, where others average out), and about 3e-3 for K = 10, since the

@@ -540,3 +540,55 @@ def test_batch_of_all_shapes_stays_within_the_bound(fs4):
         alone = fs4.muon_orthogonalize([G])[0]
         want = O.orthogonalize(np64(G))
         assert torch.equal(b, a) and far(b, want) <= NEAR + half_step(torch.bfloat16) and far(alone, want) <= NEAR + half_step(torch.bfloat16)
+
+
+@pytest.mark.parametrize("shape", [(60, 90), (20, 90), (1500, 1900)], ids=str)
+def test_updates_far_below_the_norms_floor(fs4, shape):
+    """||U|| of 1e-11 and less beside 1e-7: the iteration is a^5 = 485 times X_0, whose elements are kept
+    to 2^-37, and those of later iterates too: 485 (1 + 1/a + ...) < 700 such errors an element."""
+    for scale in (1e-12, 1e-14, 1e-17, 1e-25):
+        G = make(*shape) * scale
+        want = exact64(G)
+        got = np64(fs4.muon_orthogonalize([G.cuda()], dtype=torch.float32)[0])
+        assert np.linalg.norm(got - want) <= NEAR * np.linalg.norm(want) + 700 * 2.0 ** -37 * want.size ** 0.5
+
+
+def test_two_graphs_take_turns_in_one_workspace(fs4):
+    """Captured steps on different shapes, replayed in turn on one stream."""
+    sets = [[(100, 300), (20, 50)], [(1500, 1400)]]
+    ws = torch.zeros(max(fs4.muon_workspace_size(s) for s in sets), dtype=torch.uint8, device="cuda")
+    G = [[make(*s, torch.bfloat16).cuda() for s in shapes] for shapes in sets]
+    W, M, W2, M2 = ([[torch.zeros(s, device="cuda") for s in shapes] for shapes in sets] for _ in range(4))
+    graphs = []
+    for w, g, m in zip(W, G, M):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            fs4.muon_step(w, g, m, lr=0.1, workspace=ws)
+    for _ in range(3):
+        for graph, w, g, m in zip(graphs, W2, G, M2):
+            graph.replay()
+            fs4.muon_step(w, g, m, lr=0.1)
+    torch.cuda.synchronize()
+    for a, b in zip(W + M, W2 + M2):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("width", (24, 60, 1100))
+def test_slices_past_32_bit_offsets(fs4, width):
+    """Weights, gradient and momentum as slices of one buffer of 2.7e9 elements."""
+    rows, total = 65_500, 41_000
+    buffer = torch.zeros(rows, total, dtype=torch.bfloat16, device="cuda")
+    cut = [buffer[:, c:c + width] for c in (8, 16_001, total - width - 3)]
+    for t, k, f in zip(cut, (1, 2, 3), (2.0, 1.0, 0.5)):
+        t.copy_(make(rows, width, torch.bfloat16, k).mul(f))
+    alone = [t.clone() for t in cut]
+    last = [t[-1].clone() for t in cut]
+    fs4.muon_step(*[[t] for t in cut], lr=0.1, weight_decay=0.1)
+    fs4.muon_step(*[[t] for t in alone], lr=0.1, weight_decay=0.1)
+    assert torch.equal(cut[2], alone[2]) and torch.equal(cut[1][-1], last[1])
+    # the bound of test_slices_of_one_buffer_step_as_matrices_of_their_own, and a step of BF16 at ties
+    assert far(cut[0], np64(alone[0])) <= 2.0 ** -9 and not torch.equal(cut[0][-1], last[0])
+    assert (cut[0][-300:].float() - alone[0][-300:].float()).abs().max() <= 2.0 ** -7 * alone[0].float().abs().max()
+    for t in cut:
+        t.zero_()
+    assert not buffer.any()

@@ -422,3 +422,27 @@ def test_elements_next_to_the_largest_fp32_value(fs4):
             same(view, O.quantize(np64(x), rule), False)
             y = fs4.mxfp4_dequantize(*view, 1, 32)
             assert y[0, 0].item() == want * 2.0 ** 127 and not y[0, 1:].any(), (top, rule)
+
+
+def test_strided_operands_past_32_bit_offsets(fs4):
+    """x, D and the values read back as slices of one buffer of 2.7e9 elements."""
+    rows, total, N, K = 66_000, 41_000, 130, 260
+    buffer = torch.zeros(rows, total, dtype=torch.bfloat16, device="cuda")
+    x, d, y = buffer[:, 5:5 + K], buffer[:, 20_000:20_000 + N], buffer[:, total - K:]
+    x.copy_(make(rows, K, torch.bfloat16))
+    w = fs4.mxfp4_quantize(make(N, K, torch.float32, 3).cuda() / 64, tiled=True)
+    alone = x.clone()
+    want = fs4.mxfp4_linear(alone, w, N)
+    fs4.mxfp4_linear(x, w, N, out=d)
+    assert torch.equal(d, want)
+    a = fs4.mxfp4_quantize(x, tiled=True)
+    fs4.mxfp4_gemm(a, w, rows, N, K, out=d, accumulate=True)
+    assert torch.equal(d[-300:], fs4.mxfp4_gemm(a, w, rows, N, K, out=want, accumulate=True)[-300:]) and torch.equal(d, want)
+    for layout in (False, True):
+        view = fs4.mxfp4_quantize(x, tiled=layout)
+        fs4.mxfp4_dequantize(*view, rows, K, tiled=layout, out=y)
+        assert torch.equal(y, fs4.mxfp4_dequantize(*fs4.mxfp4_quantize(alone, tiled=layout), rows, K, tiled=layout, dtype=torch.bfloat16))
+    assert torch.equal(x, alone)
+    for t in (x, d, y):
+        t.zero_()
+    assert not buffer.any()
