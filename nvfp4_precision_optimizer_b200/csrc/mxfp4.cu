@@ -17,9 +17,10 @@
 // loads first, two threads a 32-element block) and writes the row view from registers; the column view
 // reads the tile back from shared memory, one thread a column (FP32) or a pair of columns
 // (16-bit types), and both views' scales leave as whole 512-byte atoms.  The floor is HBM: in
-// bytes per element the input's size plus 17/32 for each view.  Measured on BF16: the row view of
-// 8192 x 4096 20 us (4.3 TB/s), both views of 8192 x 5120 42 us (3.1 TB/s); stochastic 98 us, where
-// the random stream's arithmetic keeps 67% of the issue slots busy.
+// bytes per element the input's size plus 17/32 for each view.  Measured on BF16, 8192 x 5120: the row view
+// 20.6 us (5.1 TB/s); the column view 31.6 us PLAIN and 23.1 TILED, both 39.9 and 27.2 (PLAIN's column
+// view is stored in pieces of 16 bytes, half a sector, each in a row of its own); stochastic 49 us a
+// view and 94 both, where the random stream's arithmetic keeps 67% of the issue slots busy.
 #include <cstdint>
 #include <type_traits>
 
