@@ -446,3 +446,77 @@ def test_strided_operands_past_32_bit_offsets(fs4):
     for t in (x, d, y):
         t.zero_()
     assert not buffer.any()
+
+
+@pytest.mark.parametrize("size", [(1 << 20, 16, 33), (1, 1 << 20, 33), (33, 16, 1 << 20), (300, 300, 1 << 20), (1 << 20, 300, 64),
+                                  (140, 1 << 20, 96), (1, 16, 1 << 20)], ids=str)
+def test_largest_rows_columns_and_terms(fs4, size):
+    M, N, K = size
+    g = torch.Generator("cuda").manual_seed(M + N + K)
+    x, w = (torch.randn(r, K, generator=g, device="cuda", dtype=torch.float32) for r in (M, N))
+    a, b = fs4.mxfp4_quantize(x, tiled=True), fs4.mxfp4_quantize(w, tiled=True)
+    av, bv = (fs4.mxfp4_dequantize(*q, r, K, tiled=True).double() for q, r in ((a, M), (b, N)))
+    want, bound = av @ bv.T, K * 2.0 ** -23 * (av.abs() @ bv.abs().T)
+    ws = torch.zeros(fs4.mxfp4_linear_workspace_size(M, K), dtype=torch.uint8, device="cuda")
+    got = fs4.mxfp4_gemm(a, b, M, N, K, dtype=torch.float32, workspace=ws)
+    assert ((got.double() - want).abs() <= bound).all()
+    assert torch.equal(fs4.mxfp4_linear(x, b, N, workspace=ws), got) and fs4.device_status(ws) == 0
+
+
+def test_one_row_and_one_column_of_2_to_31_elements(fs4):
+    n = 1 << 31
+    x = torch.empty(1, n, dtype=torch.bfloat16, device="cuda")
+    x.copy_(torch.arange(1 << 16, device="cuda", dtype=torch.int32).remainder(97).sub(48).repeat(n >> 16)[None])
+    tail = slice(n - 4096, n)
+    codes, scales = fs4.mxfp4_quantize(x)
+    part = fs4.mxfp4_quantize(x[:, tail].contiguous())
+    assert torch.equal(codes[0, -2048:], part[0][0]) and torch.equal(scales[0, -128:], part[1][0])
+    y = fs4.mxfp4_dequantize(codes, scales, 1, n, dtype=torch.bfloat16)
+    assert torch.equal(y[:, tail], fs4.mxfp4_dequantize(*part, 1, 4096, dtype=torch.bfloat16))
+    del codes, scales, y
+    # as a column its row view has one element a row, and its column view is the row view above
+    z = x.view(n, 1)
+    codes, scales = fs4.mxfp4_quantize(z)
+    few = fs4.mxfp4_quantize(z[tail].contiguous())
+    assert torch.equal(codes[tail], few[0]) and torch.equal(scales[tail], few[1])
+    y = fs4.mxfp4_dequantize(codes, scales, n, 1, dtype=torch.bfloat16)
+    assert torch.equal(y[tail], fs4.mxfp4_dequantize(*few, 4096, 1, dtype=torch.bfloat16))
+    del codes, scales, y
+    codes, scales = fs4.mxfp4_quantize(z, axis=fs4.FS4_AXIS_COL)
+    assert torch.equal(codes[0, -2048:], part[0][0]) and torch.equal(scales[0, -128:], part[1][0])
+
+
+def test_calls_from_several_host_threads(fs4):
+    """Each thread on a stream of its own, products of all kernels and Muon steps among them."""
+    import threading
+    ops = {k: operand(fs4, 1400, 700, k)[0] for k in (1, 2)}
+    x = make(1400, 700, torch.bfloat16).cuda()
+    G = [make(300, 411, torch.bfloat16, 5).cuda(), make(1300, 1500, torch.bfloat16, 6).cuda(), make(20, 700, torch.bfloat16, 7).cuda()]
+
+    def work(i, stream=None):
+        rows = (1, 9, 100, 1400)[i % 4]
+        return [fs4.mxfp4_linear(x[:rows], ops[1], 1400, stream=stream), fs4.mxfp4_gemm(ops[1], ops[2], 1400, 1400 - 400 * (i % 3), 700, stream=stream),
+                fs4.muon_orthogonalize(G[i % 3:i % 3 + 1], stream=stream)[0], fs4.mxfp4_quantize(x[:rows], seed=i, stream=stream)[0]]
+
+    want = [work(i) for i in range(12)]
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def thread(t):
+        try:
+            stream = torch.cuda.Stream()
+            for i in range(12):
+                got[t, i] = work(i, stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=thread, args=(t,)) for t in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and len(got) == 72
+    assert all(torch.equal(a, b) for (_, i), outs in got.items() for a, b in zip(outs, want[i]))
+    assert fs4.device_status() == 0
