@@ -522,18 +522,17 @@ fs4_status fs4_root_ns_bf16_batched_timed(int32_t count, const fs4_ns_desc* desc
  *   X_0 = U / (||U||_F + 1e-7) (transposed when rows > cols), then K times
  *   A = X X^T, B = b A + c A^2, X <- a X + B X,
  * with FP16 tensor-core operands, FP32 accumulation and FP32 diagonals of A and B kept out
- * of the operands.  X is kept to 22 significand bits or to 2^-37, whichever is more (an update whose
- * norm is far below the 1e-7 beside it has a result near zero, right to that).  With the Muon
- * coefficients and K = 5 the result is 0.1-1.8e-3 (relative,
- * Frobenius) from the exact iteration, also where a few directions dominate and the rest is
- * 1e-5 of them.  It is up to 1.2e-2 where the elements of one dominant direction are all equal
- * (equal elements round alike, where others average out), and about 3e-3 for K = 10, since the
- * Muon iteration does not converge.  The same call repeats bit for bit; a matrix's bits may differ
- * with the other matrices of its call, whose sizes decide together on which kernel it runs and in how
- * many parts its Gram product is summed.  A zero matrix gives zero.  A
- * matrix with NaN or Inf in U is carried as zeros (its update is zero) and recorded as
- * FS4_ERR_NONFINITE in the status word; so is a result that is not finite, as coefficients
- * that make the iteration diverge give. */
+ * of the operands.  X is kept to 22 significand bits or to 2^-37, whichever is more (an update
+ * whose norm is far below the 1e-7 beside it has a result near zero, right to that).  With the
+ * Muon coefficients and K = 5 the result is 0.1-1.8e-3 (relative, Frobenius) from the exact
+ * iteration, also where a few directions dominate and the rest is 1e-5 of them.  It is up to
+ * 1.2e-2 where the elements of one dominant direction are all equal (equal elements round alike,
+ * where others average out), and about 3e-3 for K = 10, since the Muon iteration does not
+ * converge.  The same call repeats bit for bit; a matrix's bits may differ with the other
+ * matrices of its call, whose sizes decide together on which kernel it runs and in how many
+ * parts its Gram product is summed.  A zero matrix gives zero.  A matrix with NaN or Inf in U is
+ * carried as zeros (its update is zero) and recorded as FS4_ERR_NONFINITE in the status word; so
+ * is a result that is not finite, as coefficients that make the iteration diverge give. */
 
 enum { FS4_MUON_NESTEROV = 1u << 0 };
 
@@ -563,9 +562,9 @@ size_t fs4_muon_workspace_size(int32_t count, const int64_t* rows, const int64_t
  *   Errors: FS4_ERR_SHAPE (count outside [1, FS4_MAX_BATCH], K outside [1, FS4_MAX_ITERS], a
  *   size), FS4_ERR_INVALID_ARG (null or misaligned pointers, leading dimensions, types,
  *   coefficients, scale), FS4_ERR_ALIAS (an output overlaps an input, another output or the
- *   workspace; matrices of one pitch side by side in a buffer do not), FS4_ERR_WORKSPACE, FS4_ERR_ARCH, FS4_ERR_CUDA; FS4_ERR_NONFINITE and
- *   FS4_ERR_TIMEOUT in the status word, which each call resets.  Calls whose work overlaps on
- *   the GPU need separate workspaces. */
+ *   workspace; matrices of one pitch side by side in a buffer do not), FS4_ERR_WORKSPACE,
+ *   FS4_ERR_ARCH, FS4_ERR_CUDA; FS4_ERR_NONFINITE and FS4_ERR_TIMEOUT in the status word, which
+ *   each call resets.  Calls whose work overlaps on the GPU need separate workspaces. */
 fs4_status fs4_muon_orthogonalize(int32_t count, const fs4_muon_desc* descs, int32_t K,
                                   const float* coeffs, int32_t n_coeffs, void* workspace,
                                   size_t workspace_bytes, void* stream);
@@ -574,8 +573,9 @@ fs4_status fs4_muon_orthogonalize(int32_t count, const fs4_muon_desc* descs, int
  *   m <- beta m + (1 - beta) g         (in FP32, rounded to m's type)
  *   U = m, or with FS4_MUON_NESTEROV  beta m + (1 - beta) g  from the stored m
  *   w <- (1 - lr weight_decay) w - lr scale X_K      (in FP32, rounded to w's type)
- * lr >= 0, 0 <= beta < 1, lr and 1 - lr weight_decay within FP32.  Errors as fs4_muon_orthogonalize; a matrix with NaN or Inf keeps
- * its weights but for the decay (its momentum is updated as stated). */
+ * lr >= 0, 0 <= beta < 1, lr and 1 - lr weight_decay within FP32; flags: FS4_MUON_NESTEROV and
+ * FS4_TEST_STALL.  Errors as fs4_muon_orthogonalize; a matrix with NaN or Inf keeps its weights
+ * but for the decay (its momentum is updated as stated). */
 fs4_status fs4_muon_step(int32_t count, const fs4_muon_desc* descs, int32_t K,
                          const float* coeffs, int32_t n_coeffs, double lr, double beta,
                          double weight_decay, uint32_t flags, void* workspace,
